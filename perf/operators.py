@@ -66,9 +66,9 @@ def draw(rng):
     op = rng.choice(["linear", "linear", "linear_bwd", "glu", "glu", "glu_bwd", "clip"])
     act = rng.choice(["none", "relu", "gelu", "gelu_tanh", "silu"])
     if op == "linear":
-        dtype = rng.choice(["bf16", "f16", "fp8"])
+        dtype = rng.choice(["bf16", "f16", "fp8"])  # 8-bit layers hand 16-bit activations on
         return dict(op=op, m=_log(rng, 1, 8192), n=_wide(rng, 512, 8192) + rng.choice([0, 0, 1, 5]), k=_wide(rng, 512, 8192) // 16 * 16, dtype=dtype,
-                    out=rng.choice(["bf16", "f32"]) if dtype == "fp8" else rng.choice([dtype, "f32"]), act=act, bias=rng.random() < 0.5,
+                    out=rng.choice(["bf16", "f16"]) if dtype == "fp8" else rng.choice([dtype, "f32"]), act=act, bias=rng.random() < 0.5,
                     residual=rng.random() < 0.5, keep=rng.random() < 0.3)
     if op == "linear_bwd":
         dtype = rng.choice(["bf16", "f16"])
