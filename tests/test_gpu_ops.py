@@ -1,0 +1,503 @@
+"""The feed-forward operators on the GPU against their 64-bit definitions:
+every kernel variant (matrix-vector sized, each tile size, K split, short last
+rounds, the generic tile), every type and activation, ragged sizes, padded
+rows whose padding must be neither read (it holds NaN) nor written."""
+import itertools
+
+import pytest
+import torch
+
+from _ops_ref import ACTS, U, act, act_bound, product, rounding, slope_bound, within
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32, "fp8": torch.float8_e4m3fn}
+FP8_INNER = 7.0 * 2.0 ** -13
+MARK = 7.0  # what padding of outputs holds
+
+
+@pytest.fixture(scope="module")
+def tg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import tile_level_gemm_02_amd as tg
+
+    return tg
+
+
+@pytest.fixture(scope="module")
+def ws(tg):
+    return tg.tg_ops_workspace()
+
+
+def ld_of(cols, dtype):
+    per = 16 // dtype.itemsize
+    return -(-cols // per) * per
+
+
+def store(rows, cols, dtype, fill, extra=8):
+    """A rows x cols view whose row padding and two rows below hold `fill`."""
+    per = 16 // dtype.itemsize
+    s = torch.full((rows + 2, ld_of(cols, dtype) + extra // per * per), fill, device="cuda", dtype=torch.float32).to(dtype)
+    return s, s[:rows, :cols]
+
+
+def rand(rows, cols, dtype, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.empty(rows, cols, device="cuda").normal_(0.0, std, generator=g)
+    _, t = store(rows, cols, dtype, float("nan"), extra=16)
+    t.copy_(v.clamp(-448, 448))
+    return t
+
+
+def out(rows, cols, dtype):
+    s, t = store(rows, cols, dtype, MARK)
+    t.fill_(float("nan"))
+    return s, t
+
+
+def clean(s, rows, cols, what):
+    assert bool((s[rows:] == MARK).all()) and bool((s[:, cols:] == MARK).all()), f"{what}: wrote outside its matrix"
+
+
+def free(ws):
+    assert int(ws[: 65536 // 4].count_nonzero()) == 0, "arrival counters not zero after the call"
+
+
+def linear_case(tg, M, N, K, dt, od, name, bias, res, keep, ws, seed=1):
+    t, o = DT[dt], DT[od]
+    alpha = 0.25 if dt == "fp8" else 1.0
+    x, w = rand(M, K, t, seed), rand(N, K, t, seed + 1, K ** -0.5 * (16.0 if dt == "fp8" else 1.0))
+    b = torch.empty(N, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(seed + 2)) if bias else None
+    r = rand(M, N, o, seed + 3) if res else None
+    sy, y = out(M, N, o)
+    sz, z = out(M, N, o) if keep else (None, None)
+    print(f"linear {M}x{N}x{K} {dt}->{od} {name}", flush=True)
+    tg.tg_linear(x, w, y, bias=b, act=name, residual=r, preact=z, scale_x=0.5, scale_w=0.5, workspace=ws)
+    torch.cuda.synchronize()
+    want, tol = product(x, w, alpha, FP8_INNER if dt == "fp8" else 0.0)
+    if bias:
+        want = want + b.double()
+        tol = tol + 4 * U * want.abs() + 2 * U * b.double().abs()
+    if keep:
+        within(z, want, tol + rounding(want, o), "preact")
+        clean(sz, M, N, "preact")
+    v = act(name, want)[0]
+    tol = act_bound(name, want, v, tol)
+    if res:
+        v = v + r.double()
+        tol = tol + 2 * U * v.abs()
+    within(y, v, tol * (1 + 2.0 ** -7) + rounding(v, o), "y")
+    clean(sy, M, N, "y")
+    if ws is not None:
+        free(ws)
+
+
+# matrix-vector sized calls: one and two slices of rows, K tails, narrow N (K split over workgroups), odd N
+@pytest.mark.parametrize("M,N,K", [(1, 129, 64), (1, 256, 8192), (7, 77, 200), (8, 512, 4096), (9, 40, 72), (16, 300, 1000),
+                                   (17, 65, 136), (32, 512, 4104)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32")])
+def test_linear_few_rows(tg, ws, M, N, K, dt, od):
+    for w in (ws, None):
+        linear_case(tg, M, N, K, dt, od, "silu", True, True, True, w)
+        linear_case(tg, M, N, K, dt, od, "none", False, True, False, w)
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32"), ("fp8", "bf16"),
+                                   ("fp8", "f16"), ("fp8", "f32")])
+def test_linear_types_and_activations(tg, ws, name, dt, od):
+    for bias, res, keep in ((True, True, True), (False, False, False), (True, False, True), (False, True, False)):
+        linear_case(tg, 130, 201, 272, dt, od, name, bias, res, keep, ws)
+
+
+# each tile plan: 64 with a K split, 128, 256 x 128, 256 with five and four ring slots, a short last round in 64, 128
+# and 256 x 128 parts, and split over K; edges on every side
+@pytest.mark.parametrize("M,N,K", [(100, 520, 2048), (1270, 1281, 72), (2300, 2290, 136), (3580, 3570, 72),
+                                   (4090, 4097, 200), (4300, 4000, 72), (4400, 4600, 72), (4600, 5300, 72),
+                                   (4400, 4504, 4104)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32"), ("fp8", "bf16")])
+def test_linear_tiles(tg, ws, M, N, K, dt, od):
+    K = -(-K // 16) * 16 if dt == "fp8" else K
+    linear_case(tg, M, N, K, dt, od, "gelu", True, True, True, ws)
+
+
+# inner sizes off the 16-byte grid take the generic tile
+@pytest.mark.parametrize("M,N,K", [(1, 9, 3), (50, 70, 33), (200, 130, 257)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32"), ("fp8", "bf16")])
+def test_linear_odd_inner_sizes(tg, ws, M, N, K, dt, od):
+    linear_case(tg, M, N, K, dt, od, "gelu_tanh", True, True, True, ws)
+
+
+def test_linear_residual_in_place_and_empty(tg, ws):
+    x, w, y = rand(70, 136, torch.bfloat16, 1), rand(200, 136, torch.bfloat16, 2), rand(70, 200, torch.bfloat16, 3)
+    a = torch.empty_like(y)
+    tg.tg_linear(x, w, a, act="relu", residual=y, workspace=ws)
+    tg.tg_linear(x, w, y, act="relu", residual=y, workspace=ws)
+    assert torch.equal(a, y)
+    b = torch.randn(200, device="cuda")
+    for o in (torch.bfloat16, torch.float32):  # an empty sum
+        e = torch.full((5, 200), float("nan"), device="cuda", dtype=o)
+        tg.tg_linear(x[:5, :0], w[:, :0], e, bias=b, act="relu", workspace=ws)
+        assert torch.equal(e, b.clamp(min=0).expand(5, 200).to(o))
+    tg.tg_linear(x[:0], w, y[:0], bias=b, workspace=ws)
+
+
+def bwd_case(tg, M, N, K, dt, od, name, ws, seed=1, alias=False):
+    t, o = DT[dt], DT[od]
+    dy, x, w, z = rand(M, N, t, seed), rand(M, K, t, seed + 1), rand(N, K, t, seed + 2, K ** -0.5), rand(M, N, t, seed + 3, 2.0)
+    dy64 = dy.double()
+    sq, dz = (None, dy) if alias else out(M, N, t)
+    sx, dx = out(M, K, t)
+    sw, dw = out(N, K, o)
+    db = torch.full((N,), float("nan"), device="cuda")
+    print(f"linear_backward {M}x{N}x{K} {dt}->{od} {name}", flush=True)
+    if name == "none":
+        tg.tg_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, workspace=ws)
+        dz, want, tol = dy, dy64, torch.zeros_like(dy64)
+    else:
+        tg.tg_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, preact=z, act=name, dz=dz, workspace=ws)
+        want = dy64 * act(name, z.double())[1]
+        tol = dy64.abs() * slope_bound(name) + U * want.abs()
+        within(dz, want, tol + rounding(want, t), "dz")
+        if not alias:
+            clean(sq, M, N, "dz")
+    torch.cuda.synchronize()
+    within(db, want.sum(0), tol.sum(0) + M * U * want.abs().sum(0) + 1e-30, "dbias")
+    p, b = product(dz, w.t())
+    within(dx, p, b + rounding(p, t), "dx")
+    p, b = product(dz.t(), x.t())
+    within(dw, p, b + rounding(p, o), "dw")
+    clean(sx, M, K, "dx")
+    clean(sw, N, K, "dw")
+    if ws is not None:
+        free(ws)
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+def test_linear_backward_types_and_activations(tg, ws, name, dt, od):
+    bwd_case(tg, 203, 264, 136, dt, od, name, ws)
+    bwd_case(tg, 203, 264, 136, dt, od, name, None)
+
+
+# one token; long reductions over tokens (K split of dw); each tile of dw; sizes off the 16-byte grid
+@pytest.mark.parametrize("M,N,K", [(1, 64, 72), (2, 8, 8), (4097, 200, 136), (77, 1280, 1288), (65, 2304, 2312), (33, 3584, 3568),
+                                   (90, 4096, 4104), (40, 4400, 4008), (70, 4600, 5304), (31, 33, 70), (130, 257, 65), (65, 77, 136)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32")])
+def test_linear_backward_sizes(tg, ws, M, N, K, dt, od):
+    bwd_case(tg, M, N, K, dt, od, "gelu", ws)
+
+
+def test_linear_backward_aliases_subsets_and_empty(tg, ws):
+    bwd_case(tg, 100, 72, 136, "bf16", "bf16", "silu", ws, alias=True)
+    dy, x, w = rand(50, 64, torch.float16, 1), rand(50, 40, torch.float16, 2), rand(64, 40, torch.float16, 3)
+    full = [torch.empty(50, 40, device="cuda", dtype=torch.float16), torch.empty(64, 40, device="cuda"), torch.empty(64, device="cuda")]
+    tg.tg_linear_backward(dy, x, w, dx=full[0], dw=full[1], dbias=full[2], workspace=ws)
+    for pick in itertools.product((0, 1), repeat=3):
+        part = [torch.full_like(f, float("nan")) for f in full]
+        given = [p if k else None for p, k in zip(part, pick)]
+        tg.tg_linear_backward(dy, x, w, dx=given[0], dw=given[1], dbias=given[2], workspace=ws)
+        for p, f, k in zip(part, full, pick):
+            assert torch.equal(p, f) if k else bool(torch.isnan(p).all())
+    dw, db = torch.full((64, 40), 3.0, device="cuda"), torch.full((64,), 3.0, device="cuda")
+    tg.tg_linear_backward(dy[:0], x[:0], w, dw=dw, dbias=db, workspace=ws)
+    assert not dw.any() and not db.any()
+
+
+def glu_case(tg, M, F, D, dt, od, name, keep, ws, seed=1):
+    t, o = DT[dt], DT[od]
+    alpha = 0.25 if dt == "fp8" else 1.0
+    x, w = rand(M, D, t, seed), rand(2 * F, D, t, seed + 1, D ** -0.5 * (16.0 if dt == "fp8" else 1.0))
+    sh, h = out(M, F, o)
+    sg, gu = out(M, 2 * F, o) if keep else (None, None)
+    print(f"glu {M}x{F}x{D} {dt}->{od} {name}", flush=True)
+    tg.tg_glu(x, w, h, act=name, gate_up=gu, scale_x=0.5, scale_w=0.5, workspace=ws)
+    torch.cuda.synchronize()
+    p, b = product(x, w, alpha, FP8_INNER if dt == "fp8" else 0.0)
+    if keep:
+        within(gu, p, b + rounding(p, o), "gate_up")
+        clean(sg, M, 2 * F, "gate_up")
+    g, u, eg, eu = p[:, :F], p[:, F:], b[:, :F], b[:, F:]
+    v = act(name, g)[0]
+    ev = act_bound(name, g, v, eg)
+    y = v * u
+    within(h, y, (ev * u.abs() + (v.abs() + ev) * eu) + 2 * U * y.abs() + rounding(y, o), "h")
+    clean(sh, M, F, "h")
+    if ws is not None:
+        free(ws)
+
+
+@pytest.mark.parametrize("M,F,D", [(1, 40, 64), (1, 128, 8192), (8, 333, 520), (9, 40, 72), (16, 512, 4104), (17, 65, 136),
+                                   (32, 256, 4096)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_glu_few_rows(tg, ws, M, F, D, dt):
+    for w in (ws, None):
+        glu_case(tg, M, F, D, dt, dt, "silu", True, w)
+        glu_case(tg, M, F, D, dt, dt, "gelu", False, w)
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("fp8", "bf16"), ("fp8", "f16")])
+def test_glu_types_and_activations(tg, ws, name, dt, od):
+    for keep in (True, False):
+        glu_case(tg, 130, 200, 272, dt, od, name, keep, ws)
+
+
+@pytest.mark.parametrize("M,F,D", [(100, 260, 2048), (1270, 641, 72), (2300, 1145, 136), (3580, 1785, 72), (4090, 2049, 200),
+                                   (4300, 2000, 72), (4400, 2300, 72), (4600, 2650, 72), (4400, 2252, 4104)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("fp8", "bf16")])
+def test_glu_tiles(tg, ws, M, F, D, dt, od):
+    D = -(-D // 16) * 16 if dt == "fp8" else D
+    glu_case(tg, M, F, D, dt, od, "silu", True, ws)
+
+
+@pytest.mark.parametrize("M,F,D", [(1, 5, 3), (50, 70, 33), (200, 65, 257)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("fp8", "f16")])
+def test_glu_odd_inner_sizes(tg, ws, M, F, D, dt, od):
+    glu_case(tg, M, F, D, dt, od, "relu", True, ws)
+
+
+def glu_bwd_case(tg, M, F, D, dt, od, name, ws, seed=1, alias=False):
+    t, o = DT[dt], DT[od]
+    dy, x, wd, w = rand(M, D, t, seed), rand(M, D, t, seed + 1), rand(D, F, t, seed + 2, F ** -0.5), rand(2 * F, D, t, seed + 3, D ** -0.5)
+    gu, h = rand(M, 2 * F, t, seed + 4), rand(M, F, t, seed + 5)
+    g, u = gu[:, :F].double(), gu[:, F:].double()
+    sq, dgu = (None, gu) if alias else out(M, 2 * F, t)
+    sx, dx = out(M, D, t)
+    sw, dw = out(2 * F, D, o)
+    sd, dwd = out(D, F, o)
+    print(f"glu_backward {M}x{F}x{D} {dt}->{od} {name}", flush=True)
+    tg.tg_glu_backward(dy, wd, x, w, gu, h, dgu, dx=dx, dw_gate_up=dw, dw_down=dwd, act=name, workspace=ws)
+    torch.cuda.synchronize()
+    dh, e = product(dy, wd.t())
+    v, slope = act(name, g)
+    es, ev = slope_bound(name), act_bound(name, g, v, torch.zeros_like(g))
+    dg, du = dh * u * slope, dh * v
+    tg_, tu = (e * slope.abs() + (dh.abs() + e) * es) * u.abs() + 3 * U * dg.abs(), e * v.abs() + (dh.abs() + e) * ev + U * du.abs()
+    within(dgu, torch.cat([dg, du], 1), torch.cat([tg_ + rounding(dg, t), tu + rounding(du, t)], 1), "dgate_up")
+    p, b = product(dgu, w.t())
+    within(dx, p, b + rounding(p, t), "dx")
+    p, b = product(dgu.t(), x.t())
+    within(dw, p, b + rounding(p, o), "dw_gate_up")
+    p, b = product(dy.t(), h.t())
+    within(dwd, p, b + rounding(p, o), "dw_down")
+    if not alias:
+        clean(sq, M, 2 * F, "dgate_up")
+    clean(sx, M, D, "dx")
+    clean(sw, 2 * F, D, "dw_gate_up")
+    clean(sd, D, F, "dw_down")
+    if ws is not None:
+        free(ws)
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+def test_glu_backward_types_and_activations(tg, ws, name, dt, od):
+    glu_bwd_case(tg, 203, 264, 136, dt, od, name, ws)
+    glu_bwd_case(tg, 203, 264, 136, dt, od, name, None)
+
+
+@pytest.mark.parametrize("M,F,D", [(1, 64, 72), (3, 8, 8), (2050, 136, 200), (1270, 1288, 72), (2300, 2296, 72), (3580, 3576, 72),
+                                   (4090, 4104, 72), (4300, 4000, 72), (4400, 4504, 2056), (31, 33, 70), (130, 65, 257), (65, 136, 77)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_glu_backward_sizes(tg, ws, M, F, D, dt):
+    glu_bwd_case(tg, M, F, D, dt, dt, "silu", ws)
+
+
+def test_glu_backward_alias_and_empty(tg, ws):
+    glu_bwd_case(tg, 100, 72, 136, "bf16", "bf16", "silu", ws, alias=True)
+    t = torch.float16
+    dy, wd, x, w = rand(0, 40, t, 1), rand(40, 24, t, 2), rand(0, 40, t, 3), rand(48, 40, t, 4)
+    dw, dwd = torch.full((48, 40), 3.0, device="cuda"), torch.full((40, 24), 3.0, device="cuda")
+    tg.tg_glu_backward(dy, wd, x, w, rand(0, 48, t, 5), rand(0, 24, t, 6), rand(0, 48, t, 7), dw_gate_up=dw, dw_down=dwd, workspace=ws)
+    assert not dw.any() and not dwd.any()
+
+
+def test_gradients_against_differences(tg, ws):
+    """Directional derivatives of both layers' 64-bit definitions, by central
+    differences, against the kernels' gradients.  The kernels' 16-bit dz (or
+    [dg | du]) is rounded by half a step, 2^-11 relative to each value, and so
+    is each gradient; the differences' own error is of order step^2."""
+    t, M, N, K = torch.float16, 40, 48, 56
+    x, w = rand(M, K, t, 1), rand(N, K, t, 2, K ** -0.5)
+    c = rand(M, N, t, 3)  # the loss is sum(c * y)
+    z = (x.double() @ w.double().t().contiguous()).to(t)
+    dx, dw, dz = torch.empty(M, K, device="cuda", dtype=t), torch.empty(N, K, device="cuda"), torch.empty(M, N, device="cuda", dtype=t)
+    for name in ("gelu", "gelu_tanh", "silu"):
+        tg.tg_linear_backward(c, x, w, dx=dx, dw=dw, preact=z, act=name, dz=dz, workspace=ws)
+        for got, at in ((dx, 0), (dw, 1)):
+            v = rand(*got.shape, torch.float32, 9).double()
+            step = 1e-4
+
+            def loss(s):
+                p = [x.double(), w.double()]
+                p[at] = p[at] + s * v
+                return float((c.double() * act(name, p[0] @ p[1].t().contiguous())[0]).sum())
+
+            want = (loss(step) - loss(-step)) / (2 * step)
+            # z is rounded to 16 bits (|act''| <= 1.13 times half a step of z), dz and the gradient by half a step each
+            size = float(((c.double().abs() * 1.13) @ w.double().abs() * v.abs()).sum()) if at == 0 else \
+                float(((c.double().abs() * 1.13).t().contiguous() @ x.double().abs() * v.abs()).sum())
+            assert abs(float((got.double() * v).sum()) - want) <= 2.0 ** -11 * 3 * size + 1e-4
+    F, D = 24, 40
+    x, w, wd = rand(M, D, t, 1), rand(2 * F, D, t, 2, D ** -0.5), rand(D, F, t, 3, F ** -0.5)
+    c = rand(M, D, t, 4)
+    gu = (x.double() @ w.double().t().contiguous()).to(t)
+    for name in ("gelu", "silu"):
+        h = (act(name, gu[:, :F].double())[0] * gu[:, F:].double()).to(t)
+        dx, dw, dwd = torch.empty(M, D, device="cuda", dtype=t), torch.empty(2 * F, D, device="cuda"), torch.empty(D, F, device="cuda")
+        tg.tg_glu_backward(c, wd, x, w, gu, h, torch.empty_like(gu), dx=dx, dw_gate_up=dw, dw_down=dwd, act=name, workspace=ws)
+        p0 = [x.double(), w.double(), wd.double()]
+        g64, u64 = gu[:, :F].double(), gu[:, F:].double()
+        dh = c.double().abs() @ p0[2].abs()
+        amp = torch.cat([dh * u64.abs() * 1.13, dh * (g64.abs() + 1)], 1)  # over |dg|, |du|
+        sizes = (amp @ p0[1].abs(), amp.t().contiguous() @ p0[0].abs(), c.double().abs().t().contiguous() @ (g64.abs() * u64.abs() + 1))
+        for at, got in enumerate((dx, dw, dwd)):
+            v = rand(*got.shape, torch.float32, 9).double()
+            step = 1e-4
+
+            def loss(s):
+                p = list(p0)
+                p[at] = p[at] + s * v
+                a = p[0] @ p[1].t().contiguous()
+                return float((c.double() * ((act(name, a[:, :F])[0] * a[:, F:]) @ p[2].t().contiguous())).sum())
+
+            want = (loss(step) - loss(-step)) / (2 * step)
+            assert abs(float((got.double() * v).sum()) - want) <= 2.0 ** -11 * 4 * float((sizes[at] * v.abs()).sum()) + 1e-4
+
+
+def test_infinities_and_nan(tg, ws):
+    """A NaN or an infinity in one token reaches that token's row and no other."""
+    x, w = rand(40, 64, torch.bfloat16, 1), rand(72, 64, torch.bfloat16, 2)
+    h = torch.empty(40, 40, device="cuda", dtype=torch.bfloat16)[:, :36]
+    y = torch.empty(40, 72, device="cuda", dtype=torch.bfloat16)
+    for bad in (float("nan"), float("inf")):
+        x[3, 5] = bad
+        for name in ACTS:
+            tg.tg_linear(x, w, y, act=name, workspace=ws)
+            tg.tg_glu(x, w, h, act=name, workspace=ws)
+            for t in (y, h):
+                fine = torch.isfinite(t).all(1)
+                assert bool(fine[torch.arange(40, device="cuda") != 3].all())
+            if bad != bad:
+                assert bool(torch.isnan(y[3]).all()) and bool(torch.isnan(h[3]).all())
+
+
+# ------------------------------------------------------------------- clipping
+
+
+def clip_case(tg, sizes, types, max_norm, ws, seed=1, offset=0, std=1.0, in_place=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    grads = []
+    for n, t in zip(sizes, types):
+        buf = torch.empty(n + offset, device="cuda").normal_(0.0, std, generator=g).to(DT[t])
+        grads.append(buf[offset:])
+    before = [t.double() for t in grads]
+    outs = None if in_place else [torch.full((t.numel() + 9,), MARK, device="cuda", dtype=t.dtype) for t in grads]
+    norm = torch.full((1,), float("nan"), device="cuda")
+    tg.tg_clip_grads(grads, max_norm, out=None if in_place else [o[: t.numel()] for o, t in zip(outs, grads)], norm=norm, workspace=ws)
+    torch.cuda.synchronize()
+    want = float(sum((t.square().sum() for t in before), torch.zeros((), device="cuda", dtype=torch.float64)).sqrt())
+    assert abs(float(norm) - want) <= 2 * U * want
+    coef = min(1.0, max_norm / (want + 1e-6))
+    for k, b in enumerate(before):
+        got = grads[k] if in_place else outs[k][: b.numel()]
+        v = b * coef
+        within(got, v, 4 * U * v.abs() + rounding(v, got.dtype), f"tensor {k}")
+        if coef == 1.0:
+            assert torch.equal(got.double(), b)
+        if not in_place:
+            assert bool((outs[k][b.numel():] == MARK).all()) and torch.equal(grads[k].double(), b)
+    free(ws)
+
+
+@pytest.mark.parametrize("types", [("f32",), ("bf16",), ("f16",), ("f32", "bf16", "f16")])
+@pytest.mark.parametrize("sizes", [(1,), (7, 0, 8, 9), (8191, 8192, 8193, 16385), (100003, 3, 70001)])
+@pytest.mark.parametrize("max_norm", [0.5, 1e9, 0.0])
+def test_clip(tg, ws, types, sizes, max_norm):
+    t = [types[i % len(types)] for i in range(len(sizes))]
+    for offset in (0, 1, 8):
+        clip_case(tg, sizes, t, max_norm, ws, offset=offset)
+    clip_case(tg, sizes, t, max_norm, ws, in_place=True)
+
+
+def test_clip_many_tensors_and_large_ones(tg, ws):
+    clip_case(tg, [1 + 37 * i % 501 for i in range(1000)], ["bf16", "f32", "f16"] * 333 + ["f32"], 1.0, ws)
+    clip_case(tg, [30_000_001, 5, 17_000_000], ["bf16", "f32", "f32"], 1.0, ws)
+    clip_case(tg, [33, 44], ["f32", "f32"], 1.0, ws, std=1e25)  # squares beyond fp32's range
+
+
+def test_clip_empty_infinite_and_nan(tg, ws):
+    norm = torch.full((1,), float("nan"), device="cuda")
+    tg.tg_clip_grads([], 1.0, norm=norm, workspace=ws)
+    assert float(norm) == 0.0
+    norm.fill_(float("nan"))
+    z = torch.zeros(5, device="cuda")
+    tg.tg_clip_grads([z, z[:0]], 0.0, norm=norm, eps=0.0, workspace=ws)
+    assert float(norm) == 0.0 and not z.any()
+    for bad in (float("inf"), float("nan")):
+        a, b = torch.ones(100, device="cuda"), torch.ones(9000, device="cuda", dtype=torch.bfloat16)
+        a[7] = bad
+        tg.tg_clip_grads([a, b], 1.0, norm=norm, workspace=ws)
+        if bad != bad:
+            assert bool(torch.isnan(norm).all()) and bool(torch.isnan(a).all()) and bool(torch.isnan(b).all())
+        else:
+            assert float(norm) == bad and bool(torch.isnan(a[7])) and not b.any() and int(a.isnan().sum()) == 1
+    a = torch.full((10,), 1.0, device="cuda")
+    tg.tg_clip_grads([a], float("inf"), workspace=ws)
+    assert bool((a == 1).all())
+
+
+# ---------------------------------------------------- repeats, streams, graphs
+
+
+def _block(tg, ws, t=torch.bfloat16):
+    """One gated block's forward and backward and the clipping of its gradients, on buffers of its own."""
+    M, F, D = 333, 520, 264
+    s = {"x": rand(M, D, t, 1), "w": rand(2 * F, D, t, 2, D ** -0.5), "wd": rand(D, F, t, 3, F ** -0.5), "dy": rand(M, D, t, 4)}
+    e = {k: torch.empty(*shape, device="cuda", dtype=t) for k, shape in
+         {"h": (M, F), "gu": (M, 2 * F), "y": (M, D), "dgu": (M, 2 * F), "dx": (M, D), "dw": (2 * F, D), "dwd": (D, F), "dz": (M, D)}.items()}
+    e["db"], e["norm"], e["dw1"] = torch.empty(D, device="cuda"), torch.empty(1, device="cuda"), torch.empty(D, D, device="cuda")
+
+    def run():
+        tg.tg_glu(s["x"], s["w"], e["h"], gate_up=e["gu"], workspace=ws)
+        tg.tg_linear(e["h"], s["wd"], e["y"], residual=s["x"], workspace=ws)
+        tg.tg_glu_backward(s["dy"], s["wd"], s["x"], s["w"], e["gu"], e["h"], e["dgu"], dx=e["dx"], dw_gate_up=e["dw"],
+                           dw_down=e["dwd"], workspace=ws)
+        tg.tg_linear_backward(s["dy"], s["x"], s["wd"][:, :D].contiguous(), dw=e["dw1"], dbias=e["db"], preact=s["x"], act="gelu",
+                              dz=e["dz"], workspace=ws)
+        tg.tg_clip_grads([e["dw"], e["dwd"], e["dw1"], e["db"]], 1.0, norm=e["norm"], workspace=ws)
+
+    return s, e, run
+
+
+def test_repeats_streams_and_graph_replays_are_bit_identical(tg):
+    ws = tg.tg_ops_workspace()
+    s, e, run = _block(tg, ws)
+    run()
+    torch.cuda.synchronize()
+    first = {k: v.clone() for k, v in e.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    for k in e:
+        assert torch.equal(e[k], first[k]), f"{k} on another stream"
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for rep in range(3):
+        print(f"replay {rep}", flush=True)
+        s["x"].copy_(rand(*s["x"].shape, torch.bfloat16, 20 + rep))
+        run()
+        torch.cuda.synchronize()
+        want = {k: v.clone() for k, v in e.items()}
+        for v in e.values():
+            v.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for k in e:
+            assert torch.equal(e[k], want[k]), f"{k} in replay {rep}"
+    free(ws)

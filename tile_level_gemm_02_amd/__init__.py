@@ -22,6 +22,9 @@ Entry points (same names as the C ABI):
     tg_gemm_w4a16_ex_workspace_bytes(M, N, K)
     tg_status_string(code), tg_version()
 
+The feed-forward operators of include/tg_ops.h (tg_linear, tg_glu, their
+gradients, tg_clip_grads) are bound in ``ops.py`` and exported here too.
+
 Tensor conventions: A is M x K; for b_layout "row" B is the K x N matrix, for
 "col" B is its N x K storage (the transpose_B / nn.Linear layout); C is M x N
 and its dtype (float32, float16, bfloat16) selects the output type.  Every
@@ -306,3 +309,8 @@ def tg_dequant_w4(qweight, scales, W, K: int | None = None, group_size: int = 12
         raise ValueError("inconsistent dequant shapes")
     _ok("tg_dequant_w4", load().tg_dequant_w4(N, K, pq, ldq, ps, lds, int(group_size), int(zero_point),
                                            pw, ldw, _stream(stream)))
+
+
+from .ops import (tg_clip_grads, tg_clip_grads_workspace_bytes, tg_glu, tg_glu_backward,  # noqa: E402
+                  tg_glu_backward_workspace_bytes, tg_glu_workspace_bytes, tg_linear, tg_linear_backward,
+                  tg_linear_backward_workspace_bytes, tg_linear_workspace_bytes, tg_ops_workspace)

@@ -2,8 +2,38 @@
 // to the accumulator before the output conversion (contract in include/tg.h).
 // Both layouts of B run the NT kernel where its element grid and tile sizes
 // allow (a row-major B through transposing LDS reads), else the generic
-// tile kernel (gemm_fp8 in tg_host.hpp).
+// tile kernel.
 #include "tg_host.hpp"
+
+namespace tg {
+// fp8 GEMM (validation as for the 16-bit inputs, plus finite scales).
+tg_status gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                          int64_t ldb, int b_layout, float scale_a, float scale_b, void* C, int64_t ldc,
+                          int c_dtype, void* stream, void* ws = nullptr, int64_t ws_bytes = 0)
+{
+    bool empty;
+    tg_status st = check_dense(M, N, K, A, lda, B, ldb, b_layout, C, ldc, c_dtype, 1, &empty);
+    if (st != TG_OK || empty)
+        return st;
+    if (!__builtin_isfinite(scale_a) || !__builtin_isfinite(scale_b))
+        return TG_ERR_INVALID_VALUE;
+    TileArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.A = (const uint8_t*)A;
+    a.lda = lda;
+    a.B = (const uint8_t*)B;
+    a.ldb = ldb;
+    a.C = C;
+    a.ldc = ldc;
+    a.alpha = scale_a * scale_b;
+    hipStream_t s = (hipStream_t)stream;
+    if (b_layout == TG_COL_MAJOR)
+        return launch_dense<E_FP8, B_KCONTIG>(a, c_dtype, s, ws, ws_bytes);
+    return launch_dense<E_FP8, B_NCONTIG>(a, c_dtype, s, ws, ws_bytes);
+}
+}  // namespace tg
 
 extern "C" tg_status tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                                  const void* B, int64_t ldb, tg_layout b_layout, float scale_a,

@@ -1,0 +1,442 @@
+// Host side of the fused products (contracts in include/tg_ops.h): argument
+// checks, plans and launches, one template per operator and input type, each
+// instantiated in that type's translation unit.
+#pragma once
+
+#include <math.h>
+
+#include "tg_host.hpp"
+#include "tg_ops.h"
+
+namespace tg {
+
+// The NT tile plans and the skinny kernel's splits are those of the plain
+// GEMM of the same product; workspaces follow tg_gemm_ex's contract.
+
+inline bool act_ok(int act) { return act >= TG_ACT_NONE && act <= TG_ACT_SILU; }
+
+inline void set_act(EpiArgs& e, int act)
+{
+    e.lo = -INFINITY;
+    e.slope_lo = 1.0f;
+    e.s1 = 1.0f;
+    e.s3 = 0.0f;
+    switch (act) {
+    case TG_ACT_RELU: e.lo = 0.0f; e.slope_lo = 0.0f;  // fall through
+    case TG_ACT_NONE: e.kind = AK_CLIP; break;
+    case TG_ACT_GELU: e.kind = AK_ERF; break;
+    case TG_ACT_GELU_TANH:  // 2 sqrt(2/pi) and 0.044715 of it
+        e.s1 = 1.5957691216057308f;
+        e.s3 = 0.071354816272600245f;  // fall through
+    default: e.kind = AK_SIGMOID; break;
+    }
+}
+
+// A matrix argument of rows x cols elements; empty ones are not looked at.
+inline tg_status check_mat(const void* p, int64_t rows, int64_t cols, int64_t ld, int elem_bytes)
+{
+    if (rows == 0 || cols == 0)
+        return TG_OK;
+    if (p == nullptr || ld < cols)
+        return TG_ERR_INVALID_VALUE;
+    if (!aligned16(p) || ((ld * elem_bytes) & 15))
+        return TG_ERR_MISALIGNED;
+    return TG_OK;
+}
+
+// The workspace argument of a fused call that could use `need` bytes.
+inline tg_status check_ws(const void* ws, int64_t ws_bytes, int64_t need)
+{
+    if (ws_bytes < 0 || (ws == nullptr && ws_bytes != 0))
+        return TG_ERR_INVALID_VALUE;
+    if (ws != nullptr) {
+        if (((uintptr_t)ws & 255u) != 0)
+            return TG_ERR_MISALIGNED;
+        if (ws_bytes < need)
+            return TG_ERR_INVALID_VALUE;
+    }
+    return TG_OK;
+}
+
+template <int E> struct OutOf { static constexpr int O = E == E_F16 ? O_F16 : O_BF16; };
+
+inline void set_product(TileArgs& a, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                        int64_t ldb, void* C, int64_t ldc, float alpha)
+{
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.A = (const uint8_t*)A;
+    a.lda = lda;
+    a.B = (const uint8_t*)B;
+    a.ldb = ldb;
+    a.C = C;
+    a.ldc = ldc;
+    a.alpha = alpha;
+}
+
+// The NT kernel with both operands as k rows (a transposed A): whole 16-byte
+// chunks along M and N; offsets span one K step of rows, so K is free.
+template <int E>
+inline bool nt_eligible_tn(const TileArgs& a)
+{
+    constexpr int EB = ElemInfo<E>::bytes, CE = 16 / EB, KE = 128 / EB;
+    const int64_t lim = (int64_t)kNumRecords;
+    return a.M % CE == 0 && a.N % CE == 0 && KE * a.lda * EB + 512 < lim && KE * a.ldb * EB + 512 < lim;
+}
+
+// One product on the NT kernel where its element grid allows, else on the
+// generic tile kernel (64 x 128 tiles; for EPI_GLU 64 hidden columns).
+template <int E, int O, int BL, int EPI, int AL, class P>
+tg_status launch_fused(P& a, void* ws, int64_t ws_bytes, hipStream_t s)
+{
+    const int64_t Nt = EPI == EPI_GLU ? 2 * a.N : a.N;
+    bool nt;
+    if constexpr (AL == A_MCONTIG)
+        nt = nt_eligible_tn<E>(a);
+    else
+        nt = nt_takes<E, BL>(a);
+    if (nt) {
+        NtPlan plan = plan_nt<E, BL>(a.M, Nt, a.K, ws != nullptr);
+        if (plan.ws_bytes > ws_bytes)
+            plan = plan_nt<E, BL>(a.M, Nt, a.K, false);
+        return launch_nt_plan<E, O, BL, EPI, AL>(a, plan, ws, s);
+    }
+    const int64_t tiles = n_tiles<64, 128>(a.M, Nt);
+    if (tiles > 0x7FFFFFFF)
+        return TG_ERR_NOT_SUPPORTED;
+    a.group_m = 4;
+    hipLaunchKernelGGL((tile_gemm<E, BL, O, 64, 128, false, EPI, AL, P>), dim3((uint32_t)tiles), dim3(kThreads), 0, s,
+                       a);
+    return launched();
+}
+
+template <int E, int O, int AI, int SPLIT, int CG, int EPI>
+void launch_skinny_epi(const FusedSkinnyArgs& sa, int64_t blocks, int split, hipStream_t s)
+{
+    typedef SkinnyCfg G;
+    hipLaunchKernelGGL((skinny_gemm<E, O, G::WAVES, AI, G::RING, SPLIT, CG, EPI, FusedSkinnyArgs>),
+                       dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * G::WAVES), 0, s, sa);
+}
+
+template <int E, int O, int SPLIT>
+void launch_skinny_fused(const FusedSkinnyArgs& sa, int64_t blocks, int split, hipStream_t s)
+{
+    if (sa.M <= 8)
+        launch_skinny_epi<E, O, 1, SPLIT, 1, EPI_LINEAR>(sa, blocks, split, s);
+    else if (skinny_cg(sa.M) == 1)
+        launch_skinny_epi<E, O, 2, SPLIT, 1, EPI_LINEAR>(sa, blocks, split, s);
+    else
+        launch_skinny_epi<E, O, 2, SPLIT, 2, EPI_LINEAR>(sa, blocks, split, s);
+}
+
+template <int E, int O, int SPLIT>
+void launch_skinny_glu(const FusedSkinnyArgs& sa, int64_t blocks, int split, hipStream_t s)
+{
+    if (sa.M <= 8)
+        launch_skinny_epi<E, O, 1, SPLIT, 2, EPI_GLU>(sa, blocks, split, s);
+    else
+        launch_skinny_epi<E, O, 2, SPLIT, 2, EPI_GLU>(sa, blocks, split, s);
+}
+
+// ------------------------------------------------------------------ linear
+template <int E, int O>
+tg_status linear_out(FusedArgs& a, void* ws, int64_t ws_bytes, hipStream_t s)
+{
+    if constexpr (E != E_FP8) {
+        if (a.M <= kSkSliceMaxMSplit && a.K > 0 &&
+            skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, skinny_cg(a.M))) {
+            FusedSkinnyArgs sa{};
+            sa.M = a.M;
+            sa.N = a.N;
+            sa.K = a.K;
+            sa.A = a.A;
+            sa.lda = a.lda;
+            sa.B = a.B;
+            sa.ldb = a.ldb;
+            sa.C = a.C;
+            sa.ldc = a.ldc;
+            sa.e = a.e;
+            const int64_t blocks = skinny_blocks(a.M, a.N);
+            if (blocks > 0x7FFFFFFF)
+                return TG_ERR_NOT_SUPPORTED;
+            int split = skinny_split(blocks, a.K, false);
+            const int64_t need = split > 1 ? skinny_ws_bytes(a.M, blocks, split) : 0;
+            if (ws == nullptr || need == 0 || need > ws_bytes)
+                split = 1;
+            if (split > 1) {
+                sa.counters = (uint32_t*)ws;
+                sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+                launch_skinny_fused<E, O, 2>(sa, blocks, split, s);
+            } else {
+                launch_skinny_fused<E, O, 0>(sa, blocks, 1, s);
+            }
+            return launched();
+        }
+    }
+    return launch_fused<E, O, B_KCONTIG, EPI_LINEAR, A_KCONTIG>(a, ws, ws_bytes, s);
+}
+
+template <int E>
+tg_status linear_typed(const TileArgs& t, const EpiArgs& e, int y_dtype, void* ws, int64_t ws_bytes, void* stream)
+{
+    FusedArgs a{};
+    static_cast<TileArgs&>(a) = t;
+    a.e = e;
+    hipStream_t s = (hipStream_t)stream;
+    if (y_dtype == TG_F32)
+        return linear_out<E, O_F32>(a, ws, ws_bytes, s);
+    if constexpr (E != E_BF16)
+        if (y_dtype == TG_F16)
+            return linear_out<E, O_F16>(a, ws, ws_bytes, s);
+    if constexpr (E != E_F16)
+        if (y_dtype == TG_BF16)
+            return linear_out<E, O_BF16>(a, ws, ws_bytes, s);
+    return TG_ERR_NOT_SUPPORTED;
+}
+
+// --------------------------------------------------------------------- glu
+// The skinny kernel's launch for EPI_GLU: 16 hidden columns per workgroup.
+inline int64_t glu_skinny_blocks(int64_t M, int64_t F)
+{
+    const int64_t nblk = (F + 15) / 16, slices = (M + 15) / 16;
+    return slices == 1 ? nblk : (nblk + 7) / 8 * 8 * slices;
+}
+
+inline int64_t glu_skinny_ws_bytes(int64_t blocks, int split)
+{
+    return split <= 1 || blocks > kSplitMaxCounters ? 0 : kSplitCounterBytes + blocks * split * 2048;
+}
+
+template <int E>
+int64_t glu_ws_bytes(int64_t M, int64_t F, int64_t D)
+{
+    if (M <= 0 || F <= 0 || D <= 0 || !dims_fit(M, 2 * F, D))
+        return 0;
+    if (E != E_FP8 && M <= kSkSliceMaxMSplit) {
+        const int64_t blocks = glu_skinny_blocks(M, F);
+        return glu_skinny_ws_bytes(blocks, skinny_split(blocks, D, false));
+    }
+    return D % (16 / ElemInfo<E>::bytes) == 0 ? plan_nt<E, B_KCONTIG>(M, 2 * F, D, true).ws_bytes : 0;
+}
+
+template <int E, int O>
+tg_status glu_out(FusedArgs& a, void* ws, int64_t ws_bytes, hipStream_t s)
+{
+    if constexpr (E != E_FP8) {
+        if (a.M <= kSkSliceMaxMSplit && a.K > 0 && skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, 1)) {
+            FusedSkinnyArgs sa{};
+            sa.M = a.M;
+            sa.N = a.N;
+            sa.K = a.K;
+            sa.A = a.A;
+            sa.lda = a.lda;
+            sa.B = a.B;
+            sa.ldb = a.ldb;
+            sa.C = a.C;
+            sa.ldc = a.ldc;
+            sa.e = a.e;
+            const int64_t blocks = glu_skinny_blocks(a.M, a.N);
+            if (blocks > 0x7FFFFFFF)
+                return TG_ERR_NOT_SUPPORTED;
+            int split = skinny_split(blocks, a.K, false);
+            const int64_t need = glu_skinny_ws_bytes(blocks, split);
+            if (ws == nullptr || need == 0 || need > ws_bytes)
+                split = 1;
+            if (split > 1) {
+                sa.counters = (uint32_t*)ws;
+                sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+                launch_skinny_glu<E, O, 2>(sa, blocks, split, s);
+            } else {
+                launch_skinny_glu<E, O, 0>(sa, blocks, 1, s);
+            }
+            return launched();
+        }
+    }
+    return launch_fused<E, O, B_KCONTIG, EPI_GLU, A_KCONTIG>(a, ws, ws_bytes, s);
+}
+
+template <int E>
+tg_status glu_typed(const TileArgs& t, const EpiArgs& e, int h_dtype, void* ws, int64_t ws_bytes, void* stream)
+{
+    FusedArgs a{};
+    static_cast<TileArgs&>(a) = t;
+    a.e = e;
+    hipStream_t s = (hipStream_t)stream;
+    if constexpr (E != E_BF16)
+        if (h_dtype == TG_F16)
+            return glu_out<E, O_F16>(a, ws, ws_bytes, s);
+    if constexpr (E != E_F16)
+        if (h_dtype == TG_BF16)
+            return glu_out<E, O_BF16>(a, ws, ws_bytes, s);
+    return TG_ERR_NOT_SUPPORTED;
+}
+
+// --------------------------------------------------------------- gradients
+// dW = A^T . B with A stored K x M and B stored K x N (the reduction runs
+// over their rows): the weight gradient, in fp32 or the inputs' type.
+template <int E>
+tg_status wgrad_typed(TileArgs t, int c_dtype, void* ws, int64_t ws_bytes, void* stream)
+{
+    hipStream_t s = (hipStream_t)stream;
+    if (c_dtype == TG_F32)
+        return launch_fused<E, O_F32, B_NCONTIG, EPI_STORE, A_MCONTIG>(t, ws, ws_bytes, s);
+    return launch_fused<E, OutOf<E>::O, B_NCONTIG, EPI_STORE, A_MCONTIG>(t, ws, ws_bytes, s);
+}
+
+template <int E>
+int64_t wgrad_ws_bytes(int64_t N, int64_t K, int64_t M)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || !dims_fit(M, N, K) || N % 8 != 0 || K % 8 != 0)
+        return 0;
+    return plan_nt<E, B_NCONTIG>(N, K, M, true).ws_bytes;
+}
+
+// dh = dY . Wd with the gated block's gradient in its epilogue
+template <int E>
+tg_status glu_dgu_typed(const TileArgs& t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream)
+{
+    FusedArgs a{};
+    static_cast<TileArgs&>(a) = t;
+    a.e = e;
+    return launch_fused<E, OutOf<E>::O, B_NCONTIG, EPI_GLU_BWD, A_KCONTIG>(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+// dz = dy * act'(z), rounded to the inputs' type, and its column sums (of the
+// unrounded products, in fp32): 256 columns and a range of rows per
+// workgroup of 8 x 32 lanes, 8 consecutive columns per lane.  Bound by its
+// reads and its write.  The row ranges' partial sums meet in the workspace
+// and the last arrival adds them in range order, so that results do not
+// depend on the order of arrival.
+struct DzArgs {
+    int64_t M, N;
+    const void* dY;
+    int64_t lddy;
+    void* dZ;  // null: not written (no activation)
+    int64_t lddz;
+    float* db;  // null: no sums
+    uint32_t* counters;
+    float* partials;
+    EpiArgs e;  // R, ldr: z, or null (no activation)
+};
+
+template <int O>
+__global__ __launch_bounds__(256) void dz_colsum(DzArgs p)
+{
+    __shared__ float red[8][256];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, c8 = tid & 31u, rg = tid >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 256 + c8 * 8, left = p.N - col;
+    const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+    const bool whole = n == 8;
+    const int64_t r0 = p.M * blockIdx.y / gridDim.y, r1 = p.M * (blockIdx.y + 1) / gridDim.y;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        sum[e] = 0.0f;
+    if (n > 0)
+        for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
+            constexpr int KIND = decltype(kind)::value;
+#pragma unroll 4
+            for (int64_t r = r0 + rg; r < r1; r += 8) {
+                const u32x4 dy = load_piece<O>(p.dY, r * p.lddy + col, n, whole);
+                float d[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    d[e] = piece_value<O>(dy, e);
+                if (p.e.R != nullptr) {
+                    const u32x4 z = load_piece<O>(p.e.R, r * p.e.ldr + col, n, whole);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float value;
+                        d[e] *= act_slope<KIND>(piece_value<O>(z, e), p.e, value);
+                    }
+                }
+                if (p.dZ != nullptr) {
+                    const u32x4 q = pack_piece<O>(d);
+                    if (whole)
+                        *(u32x4*)((uint16_t*)p.dZ + r * p.lddz + col) = q;  // (read again soon: not streamed)
+                    else
+                        store_piece<O>(p.dZ, r * p.lddz + col, q, n, false);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] += d[e];
+            }
+        });
+    if (p.db == nullptr)
+        return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        red[rg][c8 * 8 + e] = sum[e];
+    __syncthreads();
+    if (tid >= 64u)
+        return;
+    f32x4 s = *(const f32x4*)&red[0][4 * lane];
+#pragma unroll
+    for (int g = 1; g < 8; ++g)
+        s += *(const f32x4*)&red[g][4 * lane];
+    const uint32_t S = gridDim.y;
+    if (S > 1u) {
+        float* const slot0 = p.partials + (size_t)blockIdx.x * S * 256;
+        splitk_store(slot0 + (size_t)blockIdx.y * 256, 0, 0, lane, s);
+        if (!splitk_last(p.counters + blockIdx.x, S, lane))
+            return;
+        s = splitk_load(slot0, 0, 0, lane);
+        for (uint32_t q0 = 1; q0 < S; q0 += 8) {
+            f32x4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (q0 + j < S)
+                    v[j] = splitk_load(slot0 + (size_t)(q0 + j) * 256, 0, 0, lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (q0 + j < S)
+                    s += v[j];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t c = (int64_t)blockIdx.x * 256 + 4 * lane + e;
+        if (c < p.N)
+            p.db[c] = s[e];
+    }
+}
+
+// Row ranges of dz_colsum: about four workgroups per compute unit, each of at
+// least 32 rows; one where the partial sums have no workspace.
+inline int64_t dz_splits(int64_t M, int64_t N)
+{
+    const int64_t blocks = (N + 255) / 256, most = (M + 31) / 32;
+    int64_t s = 1024 / blocks;
+    if (s > most)
+        s = most;
+    return s < 1 ? 1 : s;
+}
+
+inline int64_t dz_ws_bytes(int64_t M, int64_t N)
+{
+    if (M <= 0 || N <= 0 || !dims_fit(M, N, 0))
+        return 0;
+    const int64_t blocks = (N + 255) / 256, s = dz_splits(M, N);
+    return s <= 1 ? 0 : kSplitCounterBytes + blocks * s * 1024;
+}
+
+template <int E>
+tg_status dz_typed(DzArgs p, void* ws, int64_t ws_bytes, void* stream)
+{
+    const int64_t blocks = (p.N + 255) / 256;
+    int64_t splits = dz_splits(p.M, p.N);
+    if (p.db != nullptr && splits > 1) {
+        if (ws == nullptr || dz_ws_bytes(p.M, p.N) > ws_bytes) {
+            splits = 1;
+        } else {
+            p.counters = (uint32_t*)ws;
+            p.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+        }
+    }
+    hipLaunchKernelGGL((dz_colsum<OutOf<E>::O>), dim3((uint32_t)blocks, (uint32_t)splits), dim3(256), 0,
+                       (hipStream_t)stream, p);
+    return launched();
+}
+
+}  // namespace tg

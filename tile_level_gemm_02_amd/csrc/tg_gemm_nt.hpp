@@ -30,7 +30,16 @@
 //  * a row-major (N-contiguous) B is taken too (BL = B_NCONTIG): its
 //    half-stage holds the step's k rows of the tile's columns, and each B
 //    fragment comes from transposing LDS reads (ds_read_b64_tr_b16 for
-//    16-bit elements, ds_read_b64_tr_b8 for fp8).
+//    16-bit elements, ds_read_b64_tr_b8 for fp8);
+//  * so is, for 16-bit elements, a transposed A (AL = A_MCONTIG: stored K x M,
+//    the left operand of a weight gradient dz^T.x), read the same way;
+//  * fused epilogues (EPI, tg_epilogue.hpp) on the accumulator.  EPI_GLU: N
+//    is the hidden width F and B holds 2F rows, the gate's first.  A tile of
+//    BN staged columns takes BN / 2 hidden ones: staged rows come in blocks
+//    of 32, block b holding hidden columns 32 (b / 2) .. +31 of the tile, of
+//    the gate for even b and of the up projection for odd b.  Each wave's
+//    accumulator blocks 2q and 2q + 1 then hold gate and up of the same
+//    outputs, lane by lane, and the product needs no exchange.
 #pragma once
 
 #include <type_traits>
@@ -53,6 +62,17 @@ __device__ __forceinline__ i32x4_t make_rsrc(const void* base)
     const uint64_t a = (uint64_t)base;
     return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
                    __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF), kNumRecords, kBufferFlags};
+}
+
+// As make_rsrc, for a base that moves inside a loop: the copies below read
+// the descriptor from inline assembly, where the compiler does not place the
+// five wait states that a scalar register written by a vector instruction
+// (its readfirstlane) needs before a buffer instruction reads it.
+__device__ __forceinline__ i32x4_t make_rsrc_moving(const uint8_t* base)
+{
+    i32x4_t r = make_rsrc(base);
+    asm volatile("s_nop 4" : "+s"(r));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t lds_addr(uint8_t* p)
@@ -112,9 +132,12 @@ __device__ __forceinline__ void wait_copies()
 // WM x WN waves share the tile (each computes a BM/WM x BN/WN sub-tile).
 // With 8 waves (two per SIMD) the LDS sustains about twice the fragment-read
 // rate of 4 waves (one per SIMD), which the 256 x 256 tile needs.
-template <int E, int O, int BM, int BN, int RB, int NH, int WM = 2, int WN = 2, int BL = B_KCONTIG>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
+template <int E, int O, int BM, int BN, int RB, int NH, int WM = 2, int WN = 2, int BL = B_KCONTIG,
+          int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
 {
+    constexpr bool GLU = EPI == EPI_GLU;
+    constexpr int BNO = GLU ? BN / 2 : BN;  // output columns per tile
     constexpr int EB = ElemInfo<E>::bytes;
     constexpr int CE = 16 / EB;       // elements per 16-byte chunk
     constexpr int KE = RB / EB;       // K elements per step
@@ -184,6 +207,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
             return 4u * ((((k % 4u) + 1u) / 2u) % 2u);  // 128-byte rows: two rows per bank line
         }
     };
+    // M-contiguous A, likewise: RBM bytes per k row, CHM chunks
+    constexpr bool NA = AL == A_MCONTIG;
+    constexpr int RBM = BM * EB, CHM = RBM / 16, RPIM = 1024 / RBM;
+    static_assert(!NA || (EB == 2 && CHM >= 8 && (KE / RPIM) % NW == 0 && KE / RPIM / NW == AI),
+                  "M-contiguous A stage: same size and copy count as the K-contiguous one");
+    auto swm = [](uint32_t k) __attribute__((always_inline)) -> uint32_t {
+        return CHM >= 16 ? 4u * (k % 4u) : 4u * ((((k % 4u) + 1u) / 2u) % 2u);
+    };
+    static_assert(!GLU || (BL == B_KCONTIG && TN % 2 == 0 && RPI == 8 && (BN / NW == 32 || BN / NW == 64)),
+                  "gate and up blocks side by side in a wave");
 
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
 
@@ -191,7 +224,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform: keeps LDS bases scalar
     const int64_t M = p.M, N = p.N, K = p.K;
     const uint32_t tiles_m = (uint32_t)((M + BM - 1) / BM);
-    const uint32_t tiles_n = (uint32_t)((N + BN - 1) / BN);
+    const uint32_t tiles_n = (uint32_t)((N + BNO - 1) / BNO);
     // K split over S workgroups per tile (S = 1: none); this workgroup runs
     // K steps [kt0, kt0 + NK).  The ring below counts steps from kt0; global
     // offsets use the absolute step kt0 + kt.  With p.dp > 0 the first p.dp
@@ -207,14 +240,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         // sub256 - 1 on: workgroup j takes part j % Q of tile sub256 - 1 + j / Q
         constexpr uint32_t QM = 256 / BM, QN = 256 / BN, Q = QM * QN;
         static_assert(QM * BM == 256 && QN * BN == 256, "parts of a 256 x 256 tile");
-        const uint32_t tm2 = (uint32_t)((M + 255) / 256), tn2 = (uint32_t)((N + 255) / 256);
+        const uint32_t tm2 = (uint32_t)((M + 255) / 256), tn2 = (uint32_t)(GLU ? (N + 127) / 128 : (N + 255) / 256);
         const uint32_t j = xcd_remap(blockIdx.x, gridDim.x);
         uint32_t t_m, t_n;
         group_walk(p.sub256 - 1u + j / Q, tm2, tn2, p.group_m, t_m, t_n);
         tmi = t_m * QM + (j % Q) / QN;
         tni = t_n * QN + (j % Q) % QN;
         S = 1u;
-        if ((int64_t)tmi * BM >= M || (int64_t)tni * BN >= N)
+        if ((int64_t)tmi * BM >= M || (int64_t)tni * BNO >= N)
             return;  // (a part past the bottom or right edge of a partial tile)
     } else if (p.dp == 0u) {
         tile_split_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, S, p.group_m, tmi, tni, ks);
@@ -230,12 +263,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         stile = idx - ks * R;
         group_walk(p.dp + stile, tiles_m, tiles_n, p.group_m, tmi, tni);
     }
-    const int64_t m0 = (int64_t)tmi * BM, n0 = (int64_t)tni * BN;
+    const int64_t m0 = (int64_t)tmi * BM, n0 = (int64_t)tni * BNO;
     const uint32_t ldab = (uint32_t)(p.lda * EB), ldbb = (uint32_t)(p.ldb * EB);
     const int32_t rows_a = (int32_t)(M - m0 < BM ? M - m0 : BM);
-    const int32_t rows_b = (int32_t)(N - n0 < BN ? N - n0 : BN);
-    const i32x4_t ra = make_rsrc(p.A + m0 * (int64_t)ldab);
-    const i32x4_t rb = make_rsrc(NB ? p.B + n0 * EB : p.B + n0 * (int64_t)ldbb);
+    const int32_t rows_b = (int32_t)(N - n0 < BNO ? N - n0 : BNO);
+    // (GLU: rb holds the gate's rows of the tile's hidden columns and rup the
+    // up projection's; a wave that copies one block of 32 takes its own as rb)
+    constexpr bool GLU1 = GLU && BN / NW == 32;
+    const i32x4_t ra = make_rsrc(NA ? p.A + m0 * EB : p.A + m0 * (int64_t)ldab);
+    const i32x4_t rb = make_rsrc(NB ? p.B + n0 * EB : p.B + (GLU1 && (wave & 1u) ? N + n0 : n0) * (int64_t)ldbb);
+    const i32x4_t rup = make_rsrc(GLU && !GLU1 ? p.B + (N + n0) * (int64_t)ldbb : p.B);
+    // first hidden column of this wave's staged rows
+    const uint32_t glu0 = GLU1 ? (wave >> 1) * 32u : wave * 32u;
     const int64_t KT = (K + KE - 1) / KE;  // K is a multiple of CE on this path
     const int64_t kt0 = KT * ks / S, NK = KT * (ks + 1) / S - kt0;
 
@@ -256,10 +295,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
     const uint32_t lrowi = lane / CH;
     const uint32_t lchunk0 = (lane % CH) ^ ((lrowi / RSW) % CH);
     const uint32_t lchunk1 = (lane % CH) ^ ((4u + lrowi / RSW) % CH);
-    const uint32_t va0 = (wave * (BM / NW) + lrowi) * ldab + lchunk0 * 16u;
-    const uint32_t va1 = (wave * (BM / NW) + lrowi) * ldab + lchunk1 * 16u;
-    uint32_t vb0 = (wave * (BN / NW) + lrowi) * ldbb + lchunk0 * 16u;
-    uint32_t vb1 = (wave * (BN / NW) + lrowi) * ldbb + lchunk1 * 16u;
+    // (M-contiguous A: the offsets of a block of k rows, as for the
+    // N-contiguous B below)
+    const uint32_t lrowm = lane / CHM;
+    auto va_krow = [&](uint32_t q) __attribute__((always_inline)) -> uint32_t {
+        const uint32_t kr = (wave * AI + q) * RPIM + lrowm, lc = (lane % CHM) ^ swm(kr);
+        return (lrowm * ldab + lc * 16u) | (m0 + (int64_t)lc * CE < M ? 0u : kOutOfRange);
+    };
+    const uint32_t va0 = NA ? va_krow(0u) : (wave * (BM / NW) + lrowi) * ldab + lchunk0 * 16u;
+    const uint32_t va1 = NA ? va_krow(1u) : (wave * (BM / NW) + lrowi) * ldab + lchunk1 * 16u;
+    uint32_t vb0 = ((GLU ? glu0 : wave * (BN / NW)) + lrowi) * ldbb + lchunk0 * 16u;
+    uint32_t vb1 = ((GLU ? glu0 : wave * (BN / NW)) + lrowi) * ldbb + lchunk1 * 16u;
     // N-contiguous B: instruction q of wave w copies k rows (w*BI + q)*RPIN
     // + lane/CHN, lane i landing at physical chunk i%CHN of its row, which
     // holds logical chunk (i%CHN) ^ swn(row) (columns 8c .. 8c+7 of the
@@ -302,7 +348,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         o0 = (h & 1) ? vb0 : va0;
         o1 = (h & 1) ? vb1 : va1;
         if constexpr (decltype(edge)::value) {
-            if (!(NB && (h & 1))) {  // (N-contiguous B: the K tail is a row check, in copy_half)
+            if (!(NB && (h & 1)) && !(NA && !(h & 1))) {  // (k rows: the K tail is a row check, in copy_half)
                 o0 |= chunk_oob(kt0 + kt, lchunk0);
                 o1 |= chunk_oob(kt0 + kt, lchunk1);
             }
@@ -316,11 +362,39 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
     auto half_dst = [&](int64_t h) __attribute__((always_inline)) -> uint32_t {
         return lds0 + slot_of(h) + wave * ((h & 1) ? BN / NW : BM / NW) * RB;
     };
+    // Both operands as k rows (NA): the reduction runs over a long axis (the
+    // tokens of a weight gradient) whose rows can span more than a
+    // descriptor's 2 GiB, so the base moves with the step, once per half-stage,
+    // and only the step's own rows are offsets.
+    static_assert(!NA || NB, "a transposed A comes with a row-major B");
+    auto half_src = [&](int64_t h) __attribute__((always_inline)) {
+        if constexpr (NA) {
+            const int64_t k0 = (kt0 + (h >> 1)) * KE;
+            return make_rsrc_moving((h & 1) ? p.B + n0 * EB + k0 * (int64_t)ldbb : p.A + m0 * EB + k0 * (int64_t)ldab);
+        } else {
+            return 0;
+        }
+    };
     // copy instruction q of half-stage h (A of step h/2 for even h, B for odd
     // h), with the offsets o0/o1 of that half-stage
-    auto copy_half = [&](auto edge, int64_t h, int q, uint32_t o0, uint32_t o1) __attribute__((always_inline)) {
+    auto copy_half = [&](auto edge, int64_t h, int q, uint32_t o0, uint32_t o1, auto src) __attribute__((always_inline)) {
         const int64_t kt = kt0 + (h >> 1);  // absolute K step
         uint32_t v = (q & 1) ? o1 : o0;
+        if constexpr (NA) {
+            const bool b = h & 1;
+            const uint32_t kr = b ? (wave * BI + (uint32_t)q) * RPIN : (wave * AI + (uint32_t)q) * RPIM;
+            if constexpr (decltype(edge)::value)
+                v |= kt * KE + kr + (b ? lrown : lrowm) < K ? 0u : kOutOfRange;
+            load_lds_1k_at(src, half_dst(h) + q * 1024, v, kr * (b ? ldbb : ldab));
+            return;
+        }
+        if (GLU && (h & 1)) {
+            const uint32_t hq = GLU1 ? 8u * (uint32_t)q : 8u * ((uint32_t)q % 4u);  // hidden column within the block
+            if constexpr (decltype(edge)::value)
+                v |= (int32_t)(glu0 + hq + lrowi) < rows_b ? 0u : kOutOfRange;
+            load_lds_1k_at(!GLU1 && q >= 4 ? rup : rb, half_dst(h) + q * 1024, v, (uint32_t)kt * RB + hq * ldbb);
+            return;
+        }
         if (NB && (h & 1)) {  // k rows (w*BI + q)*RPIN + lane/CHN of step kt
             const uint32_t kr = (wave * BI + (uint32_t)q) * RPIN;
             if constexpr (decltype(edge)::value)
@@ -351,6 +425,24 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         const bool is_a = (r == 0) || (r > TN);
         const int idx = (r == 0) ? 0 : (r <= TN ? r - 1 : r - TN);
         const uint8_t* st = is_a ? a_ptr(kt) : b_ptr(kt);
+        if constexpr (NA) {
+            if (is_a) {
+                // as the 16-bit N-contiguous B fragments below
+                const uint32_t l16 = lane % 16u;
+                const uint32_t col = wm * (BM / WM) + (uint32_t)idx * 32u + 16u * ((lane / 16u) % 2u) + 4u * (l16 % 4u);
+                uint32_t w[4];
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2) {
+                    const uint32_t k = (uint32_t)(16 * s) + 8u * lgrp + 4u * (uint32_t)r2 + l16 / 4u;
+                    const uint32_t off = k * RBM + (((col / CE) ^ swm(k)) << 4) + (col % CE) * EB;
+                    const auto v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4_t*)(lds_u8_t)(st + off));
+                    w[2 * r2] = (uint32_t)(uint16_t)v[0] | ((uint32_t)(uint16_t)v[1] << 16);
+                    w[2 * r2 + 1] = (uint32_t)(uint16_t)v[2] | ((uint32_t)(uint16_t)v[3] << 16);
+                }
+                fa[slot][idx] = bit_cast<Frag>(u32x4{w[0], w[1], w[2], w[3]});
+                return;
+            }
+        }
         const uint32_t row0 = (is_a ? a_row0 : b_row0) + (uint32_t)idx * 32 * RB;
         Frag f;
         if constexpr (NB && EB == 1) {
@@ -473,6 +565,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         uint32_t p0, p1, r0, r1;
         half_offs(edge, 2 * kt + NH - 1, p0, p1);
         half_offs(edge, 2 * kt + NH, r0, r1);
+        const auto psrc = half_src(2 * kt + NH - 1), rsrc = half_src(2 * kt + NH);
 #pragma unroll
         for (int s = 0; s < KSTEPS - 1; ++s) {
             auto rd = [&](int r) __attribute__((always_inline)) { read_frag(kt, s + 1, (s + 1) & 1, r); };
@@ -481,7 +574,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
             // half-stage, during the second: 1-4% faster at 3072^3 .. 3584^3)
             if (s == ((NH & 1) && KSTEPS > 2 ? 1 : 0))
                 substep(s & 1, rd,
-                        [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH - 1, q, p0, p1); },
+                        [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH - 1, q, p0, p1, psrc); },
                         std::integral_constant<int, ((NH - 1) & 1) ? BI : AI>{});
             else
                 substep(s & 1, rd, nothing, std::integral_constant<int, 0>{});
@@ -492,7 +585,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         __builtin_amdgcn_sched_barrier(0);
         // (the reads of step kt+1 after the last step are stale and unused)
         substep((KSTEPS - 1) & 1, [&](int r) __attribute__((always_inline)) { read_frag(kt + 1, 0, 0, r); },
-                [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH, q, r0, r1); },
+                [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH, q, r0, r1, rsrc); },
                 std::integral_constant<int, (NH & 1) ? BI : AI>{});
     };
 
@@ -502,9 +595,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         for (int h = 0; h < NH - 1; ++h) {
             uint32_t o0, o1;
             half_offs(edge, h, o0, o1);
+            const auto src = half_src(h);
 #pragma unroll
             for (int j = 0; j < ((h & 1) ? BI : AI); ++j)
-                copy_half(edge, h, j, o0, o1);
+                copy_half(edge, h, j, o0, o1, src);
         }
         wait_copies<copies_in(2, NH - 1)>();  // step 0 landed
         __syncthreads();
@@ -514,7 +608,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
         wait_copies<0>();  // copies past the last step (zeros) must land before LDS is reused
     };
     if (NK > 0) {
-        if (rows_a == BM && rows_b == BN && K % KE == 0)  // full tiles, no K tail
+        if (rows_a == BM && rows_b == BNO && K % KE == 0)  // full tiles, no K tail
             run(std::false_type{});
         else
             run(std::true_type{});
@@ -616,14 +710,169 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(TileArgs p)
 
     // ---- epilogue
     constexpr int WR = BM / WM, WC = BN / WN;  // this wave's sub-tile
-    const int64_t wrow0 = m0 + wm * WR, wcol0 = n0 + wn * WC;
+    const int64_t wrow0 = m0 + wm * WR, wcol0 = n0 + wn * (BNO / WN);
     auto out_val = [&](int i, int j, int v) __attribute__((always_inline)) -> float {
         float x = acc[i][j][v];
         if constexpr (E == E_FP8)
             x *= p.alpha;
         return x;
     };
-    if constexpr (O == O_F32) {
+    if constexpr (EPI == EPI_GLU) {
+        // Hidden values are formed in the accumulator layout (a pair of
+        // blocks per output block), rounded to 16 bits, and staged row by row
+        // like a 16-bit output; the kept projections follow in the same LDS.
+        static_assert(O != O_F32, "16-bit hidden values");
+        constexpr int HC = WC / 2;             // hidden columns of this wave
+        constexpr int OB = HC * 2, NCH = OB / 16;
+        static_assert(NW * WR * OB <= LDS_BYTES && WR * NCH % 64 == 0, "epilogue staging");
+        uint8_t* ep = lds + wave * (WR * OB);
+        auto emit = [&](void* dst, int64_t ld, int64_t col0, bool aligned, auto val) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const uint32_t r = i * 32 + lrow;
+#pragma unroll
+                for (int j = 0; j < TN / 2; ++j) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t c = (uint32_t)(4 * j + g);
+                        *(u32x2*)(ep + r * OB + ((c ^ (r % NCH)) << 4) + lgrp * 8) =
+                            u32x2{pack2<O>(val(i, j, 4 * g), val(i, j, 4 * g + 1)),
+                                  pack2<O>(val(i, j, 4 * g + 2), val(i, j, 4 * g + 3))};
+                    }
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
+#pragma unroll
+            for (int t = 0; t < WR * NCH / 64; ++t) {
+                const uint32_t x = t * 64 + lane, r = x / NCH, c = x % NCH;
+                const u32x4 q = lds128(ep, r * OB + ((c ^ (r % NCH)) << 4));
+                const int64_t row = wrow0 + r, col = wcol0 + c * 8, left = N - col;
+                if (row < M && left > 0)
+                    store_piece<O>(dst, row * ld + col0 + col, q, left < 8 ? (int)left : 8, left >= 8 && aligned);
+            }
+        };
+        for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
+            emit(p.C, p.ldc, 0, true, [&](int i, int j, int v) __attribute__((always_inline)) {
+                return act_value<decltype(kind)::value>(out_val(i, 2 * j, v), p.e) * out_val(i, 2 * j + 1, v);
+            });
+        });
+        if (p.e.Z != nullptr) {
+            emit(p.e.Z, p.e.ldz, 0, true,
+                 [&](int i, int j, int v) __attribute__((always_inline)) { return out_val(i, 2 * j, v); });
+            emit(p.e.Z, p.e.ldz, N, N % 8 == 0,
+                 [&](int i, int j, int v) __attribute__((always_inline)) { return out_val(i, 2 * j + 1, v); });
+        }
+    } else if constexpr (EPI != EPI_STORE) {
+        // Row-wise epilogues: the fp32 accumulators go through LDS in passes
+        // of PR rows (as an fp32 output does), and come back as pieces of
+        // rows: a lane handles VC consecutive columns, the same ones in every
+        // row, so the bias is loaded once and the other operands are read and
+        // written in 16-byte pieces of whole rows.  A pass's operand loads
+        // are issued ahead of its staging.
+        constexpr int VC = Piece<O>::N;
+        constexpr int LPR = WC / VC, RPT = 64 / LPR;  // lanes per row, rows per instruction
+        constexpr int OB = WC * 4, NCH = OB / 16;
+        constexpr int PBY = LDS_BYTES / NW;
+        constexpr int PR = PBY / OB >= WR ? WR : (PBY / OB >= WR / 2 ? WR / 2 : WR / 4);
+        constexpr int NTI = PR / RPT;
+        constexpr bool BWD = EPI == EPI_GLU_BWD;
+        static_assert(PR % 32 == 0 && WR % PR == 0 && PR % RPT == 0 && 64 % LPR == 0, "staging passes");
+        uint8_t* ep = lds + wave * PBY;
+        const uint32_t ec = lane % LPR, er = lane / LPR;
+        const int64_t col = wcol0 + ec * VC, left = N - col;
+        const int n = left >= VC ? VC : left > 0 ? (int)left : 0;
+        const bool whole = n == VC, up_whole = whole && N % VC == 0;  // (BWD: the up half starts at column N)
+        float bias[VC];
+#pragma unroll
+        for (int e = 0; e < VC; ++e)
+            bias[e] = !BWD && p.e.bias != nullptr && e < n ? p.e.bias[col + e] : 0.0f;
+        // (a call per pass, not a loop: the accumulator must be indexed by constants)
+        auto run_pass = [&](auto pass_c) __attribute__((always_inline)) {
+            constexpr int pass = decltype(pass_c)::value;
+            const int64_t prow = wrow0 + pass * PR + er;
+            u32x4 r0[NTI], r1[BWD ? NTI : 1];
+            if (p.e.R != nullptr) {
+#pragma unroll
+                for (int t = 0; t < NTI; ++t) {
+                    const int64_t row = prow + t * RPT;
+                    r0[t] = u32x4{0u, 0u, 0u, 0u};
+                    if (row < M && n > 0)
+                        r0[t] = load_piece<O>(p.e.R, row * p.e.ldr + col, n, whole);
+                    if constexpr (BWD) {
+                        r1[t] = u32x4{0u, 0u, 0u, 0u};
+                        if (row < M && n > 0)
+                            r1[t] = load_piece<O>(p.e.R, row * p.e.ldr + N + col, n, up_whole);
+                    }
+                }
+            }
+#pragma unroll
+            for (int ii = 0; ii < PR / 32; ++ii) {
+                const int i = pass * (PR / 32) + ii;
+                const uint32_t r = ii * 32 + lrow;
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t c = (uint32_t)(8 * j + 2 * g) + lgrp;
+                        *(f32x4*)(ep + r * OB + ((c ^ (r % NCH)) << 4)) =
+                            f32x4{out_val(i, j, 4 * g), out_val(i, j, 4 * g + 1), out_val(i, j, 4 * g + 2),
+                                  out_val(i, j, 4 * g + 3)};
+                    }
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
+            for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
+                constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+                for (int t = 0; t < NTI; ++t) {
+                    const uint32_t r = t * RPT + er;
+                    const int64_t row = prow + t * RPT;
+                    float z[VC];
+#pragma unroll
+                    for (int h = 0; h < VC / 4; ++h) {
+                        const f32x4 q = bit_cast<f32x4>(lds128(ep, r * OB + (((ec * (VC / 4) + h) ^ (r % NCH)) << 4)));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            z[4 * h + e] = q[e];
+                    }
+                    if (row >= M || n == 0)
+                        continue;
+                    if constexpr (BWD) {
+                        float dg[VC], du[VC];
+#pragma unroll
+                        for (int e = 0; e < VC; ++e) {
+                            float value;
+                            const float slope = act_slope<KIND>(piece_value<O>(r0[t], e), p.e, value);
+                            dg[e] = z[e] * piece_value<O>(r1[t], e) * slope;
+                            du[e] = z[e] * value;
+                        }
+                        store_piece<O>(p.C, row * p.ldc + col, pack_piece<O>(dg), n, whole);
+                        store_piece<O>(p.C, row * p.ldc + N + col, pack_piece<O>(du), n, up_whole);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VC; ++e)
+                            z[e] += bias[e];
+                        if (p.e.Z != nullptr)
+                            store_piece<O>(p.e.Z, row * p.e.ldz + col, pack_piece<O>(z), n, whole);
+#pragma unroll
+                        for (int e = 0; e < VC; ++e)
+                            z[e] = act_value<KIND>(z[e], p.e);
+                        if (p.e.R != nullptr)
+#pragma unroll
+                            for (int e = 0; e < VC; ++e)
+                                z[e] += piece_value<O>(r0[t], e);
+                        store_piece<O>(p.C, row * p.ldc + col, pack_piece<O>(z), n, whole);
+                    }
+                }
+            });
+        };
+        run_pass(std::integral_constant<int, 0>{});
+        if constexpr (WR / PR >= 2)
+            run_pass(std::integral_constant<int, 1>{});
+        if constexpr (WR / PR == 4) {
+            run_pass(std::integral_constant<int, 2>{});
+            run_pass(std::integral_constant<int, 3>{});
+        }
+    } else if constexpr (O == O_F32) {
         // fp32 output: staged through LDS like the 16-bit one, so that the
         // stores are whole rows (a lane's 4 columns stored directly give 32
         // rows x 32 bytes per instruction, which measured ~50% slower for the

@@ -58,14 +58,23 @@ __device__ __forceinline__ uint32_t sk_swz(uint32_t r, uint32_t c)
 // CG: 16-column groups per workgroup (16*CG columns).  Every workgroup
 // copies its slice's A rows over all of K, so with CG = 2 the A bytes the
 // compute units copy halve, for half the workgroups.
-template <int E, int O, int WAVES, int AI, int RING, int SPLIT = 0, int CG = 1>
-__global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
+//
+// EPI: a fused epilogue (tg_epilogue.hpp) on the reduced tile.  EPI_GLU: N is
+// the hidden width F and B holds 2F rows; column group 0 is 16 gate columns
+// and group 1 the up columns of the same hidden ones, reduced by one wave.
+template <int E, int O, int WAVES, int AI, int RING, int SPLIT = 0, int CG = 1, int EPI = EPI_STORE,
+          class P = SkinnyArgs>
+__global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
 {
+    constexpr bool GLU = EPI == EPI_GLU;
+    static_assert(!GLU || CG == 2, "a gate group and an up group");
+    static_assert(EPI == EPI_STORE || SPLIT != 1, "an epilogue needs the whole sum");
     typedef typename OutInfo<O>::T OutT;
     static_assert(E == E_F16 || E == E_BF16, "16-bit inputs");
     static_assert(SPLIT != 1 || O == O_F32, "partial tiles are added in fp32");
     constexpr int SLOT = SkinnySlot<AI, CG>::BYTES;
     constexpr int COLS = 16 * CG;          // columns (B rows) per workgroup
+    constexpr int COLSO = GLU ? 16 : COLS;  // output columns per workgroup
     constexpr int BI = COLS / 8;           // B copy instructions per stage
     constexpr int PER = BI + AI;           // copy instructions per stage
     constexpr int ZERO = WAVES * RING * SLOT;  // 16 zero bytes: A rows past 8*AI
@@ -83,7 +92,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
     const int64_t S = (p.M + 15) / 16;
     const int64_t grp8 = (int64_t)blockIdx.x / (8 * S), rem = (int64_t)blockIdx.x % (8 * S);
     const int64_t slice = rem / 8;
-    const int64_t n0 = (grp8 * 8 + rem % 8) * COLS;
+    const int64_t n0 = (grp8 * 8 + rem % 8) * COLSO;
     if (n0 >= N)
         return;  // padding of the last group of eight column blocks (whole workgroup)
     const int64_t M = p.M - 16 * slice < 16 ? p.M - 16 * slice : 16;  // rows of this slice
@@ -104,11 +113,12 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
     // plus the stage offsets the ring forms, stays below 2^31.
     const i32x4_t ra = make_rsrc(Ab);
     const i32x4_t rb = make_rsrc(p.B + n0 * p.ldb * 2);
+    const i32x4_t rup = make_rsrc(GLU ? p.B + (N + n0) * p.ldb * 2 : p.B);
     uint32_t vb[BI], va[AI];
 #pragma unroll
     for (int i = 0; i < BI; ++i) {
-        const uint32_t r = 8u * i + lane / 8u;
-        vb[i] = n0 + r < N ? r * (uint32_t)p.ldb * 2u + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
+        const uint32_t r = 8u * i + lane / 8u, rr = GLU ? r % 16u : r;
+        vb[i] = n0 + rr < N ? rr * (uint32_t)p.ldb * 2u + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
     }
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
@@ -127,11 +137,11 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
         if (b_once) {
 #pragma unroll
             for (int i = 0; i < BI; ++i)
-                load_lds_1k_nt_at(rb, slot + i * 1024, vb[i] | past, soff);
+                load_lds_1k_nt_at(GLU && i >= 2 ? rup : rb, slot + i * 1024, vb[i] | past, soff);
         } else {
 #pragma unroll
             for (int i = 0; i < BI; ++i)
-                load_lds_1k_at(rb, slot + i * 1024, vb[i] | past, soff);
+                load_lds_1k_at(GLU && i >= 2 ? rup : rb, slot + i * 1024, vb[i] | past, soff);
         }
 #pragma unroll
         for (int i = 0; i < AI; ++i)
@@ -191,10 +201,10 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
             }
 #pragma unroll
             for (int g = 0; g < CG; ++g) {
-                const int64_t n = n0 + 16 * g + c16;
+                const int64_t n = n0 + (GLU ? 0 : 16 * g) + c16;
                 b = u32x4{0u, 0u, 0u, 0u};
                 if (n < N && k < K) {
-                    const uint8_t* src = p.B + (n * p.ldb + k) * 2;
+                    const uint8_t* src = p.B + ((GLU && g == 1 ? N + n : n) * p.ldb + k) * 2;
                     b = (k + 8 <= K) ? ldg128(src) : load_chunk_partial<2>(src, K - k);
                 }
                 acc[g][0] = Mfma16<E>::run(b, a, acc[g][0]);
@@ -212,6 +222,69 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(SkinnyArgs p)
         for (int v = 0; v < 4; ++v)
             red[((wave * CG + g) * 4 + v) * 64 + lane] = acc[g][0][v] + acc[g][1][v];
     __syncthreads();
+    if constexpr (EPI != EPI_STORE) {
+        if (wave < (uint32_t)(GLU ? 1 : CG)) {
+            // as below; for EPI_GLU one wave takes both groups, whose partial
+            // tiles lie side by side in its slot
+            constexpr int NG = GLU ? 2 : 1;
+            f32x4 sum[NG];
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t g = GLU ? (uint32_t)q : wave;
+                    sum[q][v] = red[(g * 4 + v) * 64 + lane];
+#pragma unroll
+                    for (int w = 1; w < WAVES; ++w)
+                        sum[q][v] += red[((w * CG + g) * 4 + v) * 64 + lane];
+                }
+            if constexpr (SPLIT == 2) {
+                constexpr int GRP = GLU ? 1 : CG;  // groups with a counter of their own
+                const uint32_t id = blockIdx.x * GRP + wave, S = gridDim.y, me = blockIdx.y;
+                float* const slot0 = p.partials + (size_t)id * S * (NG * 256);
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+                    splitk_store(slot0 + me * (NG * 256), 0, q, lane, sum[q]);
+                if (!splitk_last(p.counters + id, S, lane))
+                    return;
+                f32x4 own[NG];
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+                    own[q] = sum[q];
+                for (uint32_t s0 = 0; s0 < S; s0 += 4) {
+                    f32x4 v[4][NG];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < NG; ++q)
+                            if (s0 + j < S && s0 + j != me)
+                                v[j][q] = splitk_load(slot0 + (s0 + j) * (NG * 256), 0, q, lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s0 + j < S)
+#pragma unroll
+                            for (int q = 0; q < NG; ++q) {
+                                const f32x4 x = s0 + j == me ? own[q] : v[j][q];
+                                sum[q] = s0 + j == 0u ? x : sum[q] + x;
+                            }
+                }
+            }
+            const int64_t row = 16 * slice + c16, col0 = n0 + (GLU ? 0 : 16 * wave) + 4 * h;
+            if ((int64_t)c16 < M)
+                for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
+                    constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (col0 + v < N) {
+                            if constexpr (GLU)
+                                glu_value<O, KIND>(p.e, p.C, p.ldc, N, row, col0 + v, sum[0][v], sum[1][v]);
+                            else
+                                linear_value<O, KIND>(p.e, p.C, p.ldc, row, col0 + v, sum[0][v]);
+                        }
+                });
+        }
+        return;
+    }
     if (wave < (uint32_t)CG) {  // wave g sums column group g over the K split, in wave order
         const uint32_t g = wave;
         OutT* C = (OutT*)p.C + 16 * slice * p.ldc;

@@ -1,0 +1,11 @@
+// The fused products of include/tg_ops.h for bf16 inputs: tg_glu.
+#include "tg_fused.hpp"
+
+namespace tg {
+tg_status glu_bf16(const TileArgs& t, const EpiArgs& e, int h_dtype, void* ws, int64_t ws_bytes, void* stream)
+{
+    return glu_typed<E_BF16>(t, e, h_dtype, ws, ws_bytes, stream);
+}
+
+int64_t glu_ws_bytes_bf16(int64_t M, int64_t F, int64_t D) { return glu_ws_bytes<E_BF16>(M, F, D); }
+}  // namespace tg

@@ -364,24 +364,30 @@ NtPlan plan_nt(int64_t M, int64_t N, int64_t K, bool allow_split)
     return p;
 }
 
-template <int E, int O, int BM, int BN, int BL, int NH>
-tg_status launch_nt(const TileArgs& a, int splits, hipStream_t s, int64_t grid_override = 0)
+// (EPI, AL, P: a fused epilogue and a transposed A, see gemm_nt.  EPI_GLU
+// stages 2 N columns; its 64 tile runs 2 waves of 32 x 64, so that each wave
+// holds a gate block and the up block beside it.)
+template <int E, int O, int BM, int BN, int BL, int NH, int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
+tg_status launch_nt(const P& a, int splits, hipStream_t s, int64_t grid_override = 0)
 {
-    const int64_t tiles = n_tiles<BM, BN>(a.M, a.N);
+    const int64_t tiles = n_tiles<BM, BN>(a.M, EPI == EPI_GLU ? 2 * a.N : a.N);
     const int64_t grid = grid_override > 0 ? grid_override : a.dp > 0 ? a.dp + (tiles - a.dp) * splits : tiles * splits;
     if (grid > 0x7FFFFFFF)
         return TG_ERR_NOT_SUPPORTED;
     constexpr int RB = NtStaging<E>::RB;
-    constexpr int WM = NtWaves<E, BM, BN>::WM, WN = NtWaves<E, BM, BN>::WN;
-    hipLaunchKernelGGL((gemm_nt<E, O, BM, BN, RB, NH, WM, WN, BL>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, s, a);
+    constexpr int WM = NtWaves<E, BM, BN>::WM, WN = EPI == EPI_GLU && BN == 64 ? 1 : NtWaves<E, BM, BN>::WN;
+    hipLaunchKernelGGL((gemm_nt<E, O, BM, BN, RB, NH, WM, WN, BL, EPI, AL, P>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, s, a);
     return launched();
 }
 
 // Launch an NT plan.  With plan.splits > 1, `ws` is a zeroed-counter
 // workspace of at least plan.ws_bytes bytes (256-byte aligned).
-template <int E, int O, int BL>
-tg_status launch_nt_plan(TileArgs& a, const NtPlan& plan, void* ws, hipStream_t s)
+template <int E, int O, int BL, int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
+tg_status launch_nt_plan(P& a, const NtPlan& plan, void* ws, hipStream_t s)
 {
+    // (a transposed A keeps four ring slots: with five the moving bases of both
+    // operands do not fit the registers, 41 spills)
+    constexpr int NH5 = AL == A_MCONTIG ? 4 : 5;
     a.group_m = 4;
     a.splits = (uint32_t)plan.splits;
     a.dp = (uint32_t)plan.dp;
@@ -392,44 +398,44 @@ tg_status launch_nt_plan(TileArgs& a, const NtPlan& plan, void* ws, hipStream_t 
     if (plan.tail != kTailNone) {
         // the first plan.dp tiles of 256 x 256 whole, then every later tile of
         // the walk in parts, in a second launch
-        const int64_t rest = n_tiles<256, 256>(a.M, a.N) - plan.dp;
-        TileArgs b = a;
+        const int64_t rest = n_tiles<256, 256>(a.M, EPI == EPI_GLU ? 2 * a.N : a.N) - plan.dp;
+        P b = a;
         a.dp = (uint32_t)plan.dp;
-        tg_status st = plan.nh == 5 ? launch_nt<E, O, 256, 256, BL, 5>(a, 1, s, plan.dp)
-                                    : launch_nt<E, O, 256, 256, BL, 4>(a, 1, s, plan.dp);
+        tg_status st = plan.nh == 5 ? launch_nt<E, O, 256, 256, BL, NH5, EPI, AL>(a, 1, s, plan.dp)
+                                    : launch_nt<E, O, 256, 256, BL, 4, EPI, AL>(a, 1, s, plan.dp);
         if (st != TG_OK)
             return st;
         b.dp = 0;
         b.splits = 1;
         b.sub256 = (uint32_t)plan.dp + 1u;
         if (plan.tail == kTailWide)
-            return launch_nt<E, O, 256, 128, BL, kWideNH>(b, 1, s, 2 * rest);
+            return launch_nt<E, O, 256, 128, BL, kWideNH, EPI, AL>(b, 1, s, 2 * rest);
         if (plan.tail == kTail128)
-            return launch_nt<E, O, 128, 128, BL, 8>(b, 1, s, 4 * rest);
+            return launch_nt<E, O, 128, 128, BL, 8, EPI, AL>(b, 1, s, 4 * rest);
         if constexpr (ElemInfo<E>::bytes == 1 && BL == B_NCONTIG)
             return TG_ERR_NOT_SUPPORTED;  // (never planned)
         else
-            return launch_nt<E, O, 64, 64, BL, 8>(b, 1, s, 16 * rest);
+            return launch_nt<E, O, 64, 64, BL, 8, EPI, AL>(b, 1, s, 16 * rest);
     }
     if (plan.tile == 256 && plan.tn == 128) {
         if (plan.nh == 6)
-            return launch_nt<E, O, 256, 128, BL, 6>(a, plan.splits, s);
-        return launch_nt<E, O, 256, 128, BL, 4>(a, plan.splits, s);
+            return launch_nt<E, O, 256, 128, BL, 6, EPI, AL>(a, plan.splits, s);
+        return launch_nt<E, O, 256, 128, BL, 4, EPI, AL>(a, plan.splits, s);
     }
     if (plan.tile == 256) {
         if (plan.nh == 5)
-            return launch_nt<E, O, 256, 256, BL, 5>(a, plan.splits, s);
-        return launch_nt<E, O, 256, 256, BL, 4>(a, plan.splits, s);
+            return launch_nt<E, O, 256, 256, BL, NH5, EPI, AL>(a, plan.splits, s);
+        return launch_nt<E, O, 256, 256, BL, 4, EPI, AL>(a, plan.splits, s);
     }
     if (plan.tile == 128) {
         if (plan.nh == 8)
-            return launch_nt<E, O, 128, 128, BL, 8>(a, plan.splits, s);
-        return launch_nt<E, O, 128, 128, BL, 4>(a, plan.splits, s);
+            return launch_nt<E, O, 128, 128, BL, 8, EPI, AL>(a, plan.splits, s);
+        return launch_nt<E, O, 128, 128, BL, 4, EPI, AL>(a, plan.splits, s);
     }
     if constexpr (ElemInfo<E>::bytes == 1 && BL == B_NCONTIG)
         return TG_ERR_NOT_SUPPORTED;  // (never planned: 64-byte fp8 B rows)
     else
-        return launch_nt<E, O, 64, 64, BL, 8>(a, plan.splits, s);
+        return launch_nt<E, O, 64, 64, BL, 8, EPI, AL>(a, plan.splits, s);
 }
 
 // Whether the NT kernel takes this problem, for either layout of B.
@@ -636,34 +642,6 @@ tg_status gemm_16bit(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
     if (b_layout == TG_COL_MAJOR)
         return launch_dense<E, B_KCONTIG>(a, c_dtype, s, ws, ws_bytes);
     return launch_dense<E, B_NCONTIG>(a, c_dtype, s, ws, ws_bytes);
-}
-
-// fp8 GEMM (validation as for the 16-bit inputs, plus finite scales).
-inline tg_status gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
-                          int64_t ldb, int b_layout, float scale_a, float scale_b, void* C, int64_t ldc,
-                          int c_dtype, void* stream, void* ws = nullptr, int64_t ws_bytes = 0)
-{
-    bool empty;
-    tg_status st = check_dense(M, N, K, A, lda, B, ldb, b_layout, C, ldc, c_dtype, 1, &empty);
-    if (st != TG_OK || empty)
-        return st;
-    if (!__builtin_isfinite(scale_a) || !__builtin_isfinite(scale_b))
-        return TG_ERR_INVALID_VALUE;
-    TileArgs a{};
-    a.M = M;
-    a.N = N;
-    a.K = K;
-    a.A = (const uint8_t*)A;
-    a.lda = lda;
-    a.B = (const uint8_t*)B;
-    a.ldb = ldb;
-    a.C = C;
-    a.ldc = ldc;
-    a.alpha = scale_a * scale_b;
-    hipStream_t s = (hipStream_t)stream;
-    if (b_layout == TG_COL_MAJOR)
-        return launch_dense<E_FP8, B_KCONTIG>(a, c_dtype, s, ws, ws_bytes);
-    return launch_dense<E_FP8, B_NCONTIG>(a, c_dtype, s, ws, ws_bytes);
 }
 
 // Workspace a dense call would use for its K split: the skinny kernel's for

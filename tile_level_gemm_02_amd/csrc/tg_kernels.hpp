@@ -11,6 +11,7 @@
 #pragma once
 
 #include "tg_device.hpp"
+#include "tg_epilogue.hpp"
 
 namespace tg {
 
@@ -49,8 +50,15 @@ struct TileArgs {
     uint32_t sub256;
 };
 
+// arguments of a product with a fused epilogue
+struct FusedArgs : TileArgs {
+    EpiArgs e;
+};
+
 // B storage: K-contiguous (column-major K x N, i.e. N x K rows) or N-contiguous
 enum BLay : int { B_KCONTIG = 0, B_NCONTIG = 1 };
+// A storage: K-contiguous (M x K rows) or M-contiguous (the transpose: K x M rows)
+enum ALay : int { A_KCONTIG = 0, A_MCONTIG = 1 };
 
 constexpr int kThreads = 256;  // 4 waves, arranged 2 x 2 over the output tile
 
@@ -62,10 +70,20 @@ constexpr int kThreads = 256;  // 4 waves, arranged 2 x 2 over the output tile
 // buffer, the 128-bit global loads of the next K step are in flight in
 // registers; they are written to the other buffer after the MFMAs, then one
 // barrier flips the buffers.
+//
+// EPI selects a fused epilogue (P = FusedArgs), AL a transposed A; such calls
+// come here only where their sizes keep them off the NT kernel.  For EPI_GLU
+// N is the hidden width F and B holds 2F rows, the gate's first: a tile of BN
+// staged columns takes BN / 2 hidden ones, blocks of 32 alternating between
+// gate and up (block b: hidden columns 32 (b / 2) .. +31 of the tile, of the
+// gate for even b).
 // --------------------------------------------------------------------------
-template <int E, int BL, int O, int BM, int BN, bool W4>
-__global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
+template <int E, int BL, int O, int BM, int BN, bool W4, int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
+__global__ __launch_bounds__(kThreads) void tile_gemm(P p)
 {
+    constexpr bool GLU = EPI == EPI_GLU;
+    constexpr int BNO = GLU ? BN / 2 : BN;  // output columns per tile
+    static_assert(!GLU || (BL == B_KCONTIG && BN % 128 == 0), "gate and up blocks of a wave side by side");
     constexpr int EB = ElemInfo<E>::bytes;
     constexpr int CE = 16 / EB;   // elements per 16-byte chunk
     constexpr int KE = 128 / EB;  // K elements per step
@@ -86,11 +104,11 @@ __global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
     const uint32_t wave = tid >> 6;
     const int64_t M = p.M, N = p.N, K = p.K;
     const uint32_t tiles_m = (uint32_t)((M + BM - 1) / BM);
-    const uint32_t tiles_n = (uint32_t)((N + BN - 1) / BN);
+    const uint32_t tiles_n = (uint32_t)((N + BNO - 1) / BNO);
     uint32_t tmi, tni;
     tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, p.group_m, tmi, tni);
     const int64_t m0 = (int64_t)tmi * BM;
-    const int64_t n0 = (int64_t)tni * BN;
+    const int64_t n0 = (int64_t)tni * BNO;
     const int64_t KT = (K + KE - 1) / KE;
 
     u32x4 ra[A_CH];
@@ -100,6 +118,22 @@ __global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
 
     // ---- global -> registers, one K step
     auto load_a = [&](int64_t kt) {
+        if constexpr (AL == A_MCONTIG) {
+            constexpr int MCH = BM / CE;  // chunks along one row of the transpose (fixed k)
+#pragma unroll
+            for (int i = 0; i < A_CH; ++i) {
+                const uint32_t idx = tid + kThreads * i;
+                const int64_t gk = kt * KE + idx / MCH;
+                const int64_t gm = m0 + (int64_t)(idx % MCH) * CE;
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (gk < K && gm < M) {
+                    const uint8_t* src = p.A + (gk * p.lda + gm) * EB;
+                    v = (gm + CE <= M) ? ldg128(src) : load_chunk_partial<EB>(src, M - gm);
+                }
+                ra[i] = v;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < A_CH; ++i) {
             const uint32_t idx = tid + kThreads * i;
@@ -132,11 +166,17 @@ __global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
 #pragma unroll
             for (int i = 0; i < B_CH; ++i) {
                 const uint32_t idx = tid + kThreads * i;
-                const int64_t gn = n0 + (idx >> 3);
+                int64_t gn = n0 + (idx >> 3);
                 const int64_t gk = kt * KE + (int64_t)(idx & 7u) * CE;
                 u32x4 v = {0u, 0u, 0u, 0u};
+                int64_t row = gn;
+                if constexpr (GLU) {
+                    const uint32_t r = idx >> 3, blk = r >> 5;
+                    gn = n0 + (blk >> 1) * 32 + (r & 31u);  // hidden column
+                    row = (blk & 1u) ? N + gn : gn;
+                }
                 if (gn < N && gk < K) {
-                    const uint8_t* src = p.B + (gn * p.ldb + gk) * EB;
+                    const uint8_t* src = p.B + (row * p.ldb + gk) * EB;
                     v = (gk + CE <= K) ? ldg128(src) : load_chunk_partial<EB>(src, K - gk);
                 }
                 rb[i] = v;
@@ -161,10 +201,29 @@ __global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
     auto store_ab = [&](int buf) {
         uint8_t* As = smem + buf * (BM + BN) * 128;
         uint8_t* Bs = As + BM * 128;
+        if constexpr (AL == A_MCONTIG) {
+            // transpose on the way in, as a row-major B below
+            constexpr int MCH = BM / CE;
 #pragma unroll
-        for (int i = 0; i < A_CH; ++i) {
-            const uint32_t idx = tid + kThreads * i;
-            sts128(As, swz(idx >> 3, idx & 7u), ra[i]);
+            for (int i = 0; i < A_CH; ++i) {
+                const uint32_t idx = tid + kThreads * i;
+                const uint32_t kbyte = idx / MCH * EB, mb = (idx % MCH) * CE;
+#pragma unroll
+                for (int e = 0; e < CE; ++e) {
+                    const uint32_t v = ra[i][(e * EB) >> 2] >> (((e * EB) & 3) * 8);
+                    const uint32_t off = swz(mb + e, kbyte >> 4) + (kbyte & 15u);
+                    if constexpr (EB == 2)
+                        *(uint16_t*)(As + off) = (uint16_t)v;
+                    else
+                        *(uint8_t*)(As + off) = (uint8_t)v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < A_CH; ++i) {
+                const uint32_t idx = tid + kThreads * i;
+                sts128(As, swz(idx >> 3, idx & 7u), ra[i]);
+            }
         }
         if constexpr (W4) {
             const W4Consts wc = w4_consts(p.zero_point);
@@ -276,6 +335,33 @@ __global__ __launch_bounds__(kThreads) void tile_gemm(TileArgs p)
 
     // ---- epilogue: accumulator block (32x32, 16 values per lane) -> C
     // value v of lane l sits at row 8*(v/4) + 4*(l/32) + v%4, column l%32
+    if constexpr (EPI != EPI_STORE) {
+        const float alpha = E == E_FP8 ? p.alpha : 1.0f;
+        for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
+            constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < TN; j += GLU ? 2 : 1) {
+                    const int64_t col = n0 + (GLU ? (rowB0 + j * 32) / 2 : rowB0 + j * 32) + lrow;
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const int64_t row = m0 + rowA0 + i * 32 + (v >> 2) * 8 + lgrp * 4 + (v & 3);
+                        if (row < M && col < N) {
+                            if constexpr (EPI == EPI_LINEAR)
+                                linear_value<O, KIND>(p.e, p.C, p.ldc, row, col, acc[i][j][v] * alpha);
+                            else if constexpr (EPI == EPI_GLU)
+                                glu_value<O, KIND>(p.e, p.C, p.ldc, N, row, col, acc[i][j][v] * alpha,
+                                                   acc[i][j + 1][v] * alpha);
+                            else
+                                glu_bwd_value<O, KIND>(p.e, p.C, p.ldc, N, row, col, acc[i][j][v]);
+                        }
+                    }
+                }
+            }
+        });
+        return;
+    }
     OutT* C = (OutT*)p.C;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -312,6 +398,11 @@ struct SkinnyArgs {
     // counter per workgroup column, one 1 KiB partial tile per workgroup
     uint32_t* counters;
     float* partials;
+};
+
+// with a fused epilogue (EPI_LINEAR, EPI_GLU)
+struct FusedSkinnyArgs : SkinnyArgs {
+    EpiArgs e;
 };
 
 template <int E> struct Mfma16;
