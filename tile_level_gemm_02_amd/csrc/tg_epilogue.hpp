@@ -258,4 +258,190 @@ __device__ __forceinline__ void glu_bwd_value(const EpiArgs& e, void* C, int64_t
     store_value<O>(C, row * ldc + F + col, dh * value);
 }
 
+// ------------------------------------------------- epilogues of a wave's tile
+// A wave's WR x WC accumulator tile as quads: 4 consecutive columns of one
+// row per lane.  Row block i holds RBK rows (32 or 16, the matrix
+// instruction's), this lane's being row lane % RBK; its quad q covers columns
+// q * 4G + 4 (lane / RBK) .. +3 with G = 64 / RBK lanes side by side.
+// `get(i, q)` returns a quad, scaled; i and q are constants after unrolling.
+
+// Round to 16 bits, stage the wave's rows in its own LDS region `ep`
+// (XOR-swizzled 16-byte chunks) and store whole rows: `NQ` quads per row
+// block, of columns col0 .. of an M x N matrix `dst` from row0 on, shifted by
+// `shift` columns; `aligned`: 16-byte pieces of the shifted rows are aligned.
+template <int O, int RBK, int WR, int HC, class Get>
+__device__ __forceinline__ void store_rows16(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                             void* dst, int64_t ld, int64_t shift, bool aligned, Get get)
+{
+    constexpr int G = 64 / RBK, NQ = HC / (4 * G);
+    constexpr int OB = HC * 2, NCH = OB / 16;
+    static_assert(WR % RBK == 0 && HC % (4 * G) == 0 && (WR * NCH) % 64 == 0, "staging shape");
+    const uint32_t lr = lane % RBK, lg = lane / RBK;
+#pragma unroll
+    for (int i = 0; i < WR / RBK; ++i) {
+        const uint32_t r = i * RBK + lr;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const f32x4 v = get(i, q);
+            const uint32_t b = (q * 4 * G + 4 * lg) * 2;  // byte of the quad in its row
+            *(u32x2*)(ep + r * OB + (((b >> 4) ^ (r % NCH)) << 4) + (b & 8u)) = u32x2{pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3])};
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
+#pragma unroll
+    for (int t = 0; t < WR * NCH / 64; ++t) {
+        const uint32_t x = t * 64 + lane, r = x / NCH, c = x % NCH;
+        const u32x4 q = lds128(ep, r * OB + ((c ^ (r % NCH)) << 4));
+        const int64_t row = row0 + r, col = col0 + c * 8, left = N - col;
+        if (row < M && left > 0)
+            store_piece<O>(dst, row * ld + shift + col, q, left < 8 ? (int)left : 8, left >= 8 && aligned);
+    }
+}
+
+// EPI_GLU: hidden values are formed in the accumulator layout (the gate's
+// and the up projection's 32-column blocks alternate), rounded to 16 bits and
+// stored by rows; the kept projections follow through the same LDS.
+template <int O, int RBK, int WR, int WC, class Get>
+__device__ __forceinline__ void glu_epilogue(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, int64_t M, int64_t F,
+                                             void* C, int64_t ldc, const EpiArgs& e, Get get)
+{
+    static_assert(O != O_F32, "16-bit hidden values");
+    constexpr int G = 64 / RBK, QB = 32 / (4 * G);  // quads per 32-column block
+    for_act_kind(e.kind, [&](auto kind) __attribute__((always_inline)) {
+        store_rows16<O, RBK, WR, WC / 2>(ep, lane, row0, col0, M, F, C, ldc, 0, true, [&](int i, int q) __attribute__((always_inline)) {
+            const f32x4 g = get(i, q / QB * 2 * QB + q % QB), u = get(i, (q / QB * 2 + 1) * QB + q % QB);
+            f32x4 h;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                h[x] = act_value<decltype(kind)::value>(g[x], e) * u[x];
+            return h;
+        });
+    });
+    if (e.Z != nullptr) {
+        store_rows16<O, RBK, WR, WC / 2>(ep, lane, row0, col0, M, F, e.Z, e.ldz, 0, true, [&](int i, int q) __attribute__((always_inline)) {
+            return get(i, q / QB * 2 * QB + q % QB);
+        });
+        store_rows16<O, RBK, WR, WC / 2>(ep, lane, row0, col0, M, F, e.Z, e.ldz, F, F % 8 == 0,
+                                         [&](int i, int q) __attribute__((always_inline)) {
+                                             return get(i, (q / QB * 2 + 1) * QB + q % QB);
+                                         });
+    }
+}
+
+// EPI_LINEAR, EPI_GLU_BWD and fp32 EPI_STORE: the fp32 accumulators go
+// through LDS (PBY bytes of this wave's own) in passes of PR rows, and come
+// back as pieces of rows: a lane handles VC consecutive columns, the same
+// ones in every row, so the bias is loaded once and the other operands are
+// read and written in 16-byte pieces of whole rows.  A pass's operand loads
+// are issued ahead of its staging.
+template <int O, int EPI, int RBK, int WR, int WC, int PBY, class Get>
+__device__ __forceinline__ void rows_epilogue(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                              void* C, int64_t ldc, const EpiArgs& ea, Get get)
+{
+    constexpr int G = 64 / RBK, NQ = WC / (4 * G);
+    constexpr int VC = Piece<O>::N;
+    constexpr int LPR = WC / VC, RPT = 64 / LPR;  // lanes per row, rows per instruction
+    constexpr int OB = WC * 4, NCH = OB / 16;
+    constexpr int PR = PBY / OB >= WR ? WR : (PBY / OB >= WR / 2 ? WR / 2 : WR / 4);
+    constexpr int NTI = PR / RPT;
+    constexpr bool BWD = EPI == EPI_GLU_BWD, LIN = EPI == EPI_LINEAR;
+    static_assert(PR % RBK == 0 && WR % PR == 0 && PR % RPT == 0 && 64 % LPR == 0 && PR * OB <= PBY, "staging passes");
+    const uint32_t ec = lane % LPR, er = lane / LPR;
+    const int64_t col = col0 + ec * VC, left = N - col;
+    const int n = left >= VC ? VC : left > 0 ? (int)left : 0;
+    const bool whole = n == VC, up_whole = whole && N % VC == 0;  // (BWD: the up half starts at column N)
+    const void* const R = EPI == EPI_STORE ? nullptr : ea.R;
+    float bias[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e)
+        bias[e] = LIN && ea.bias != nullptr && e < n ? ea.bias[col + e] : 0.0f;
+    // (a call per pass, not a loop: the accumulator must be indexed by constants)
+    auto run_pass = [&](auto pass_c) __attribute__((always_inline)) {
+        constexpr int pass = decltype(pass_c)::value;
+        const int64_t prow = row0 + pass * PR + er;
+        u32x4 r0[NTI], r1[BWD ? NTI : 1];
+        if (R != nullptr) {
+#pragma unroll
+            for (int t = 0; t < NTI; ++t) {
+                const int64_t row = prow + t * RPT;
+                r0[t] = u32x4{0u, 0u, 0u, 0u};
+                if (row < M && n > 0)
+                    r0[t] = load_piece<O>(R, row * ea.ldr + col, n, whole);
+                if constexpr (BWD) {
+                    r1[t] = u32x4{0u, 0u, 0u, 0u};
+                    if (row < M && n > 0)
+                        r1[t] = load_piece<O>(R, row * ea.ldr + N + col, n, up_whole);
+                }
+            }
+        }
+#pragma unroll
+        for (int ii = 0; ii < PR / RBK; ++ii) {
+            const uint32_t r = ii * RBK + lane % RBK;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const uint32_t c = q * G + lane / RBK;  // 16-byte chunk of the quad
+                *(f32x4*)(ep + r * OB + ((c ^ (r % NCH)) << 4)) = get(pass * (PR / RBK) + ii, q);
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
+        auto finish = [&](auto kind) __attribute__((always_inline)) {
+            constexpr int KIND = decltype(kind)::value;
+#pragma unroll
+            for (int t = 0; t < NTI; ++t) {
+                const uint32_t r = t * RPT + er;
+                const int64_t row = prow + t * RPT;
+                float z[VC];
+#pragma unroll
+                for (int h = 0; h < VC / 4; ++h) {
+                    const f32x4 q = bit_cast<f32x4>(lds128(ep, r * OB + (((ec * (VC / 4) + h) ^ (r % NCH)) << 4)));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[4 * h + e] = q[e];
+                }
+                if (row >= M || n == 0)
+                    continue;
+                if constexpr (BWD) {
+                    float dg[VC], du[VC];
+#pragma unroll
+                    for (int e = 0; e < VC; ++e) {
+                        float value;
+                        const float slope = act_slope<KIND>(piece_value<O>(r0[t], e), ea, value);
+                        dg[e] = z[e] * piece_value<O>(r1[t], e) * slope;
+                        du[e] = z[e] * value;
+                    }
+                    store_piece<O>(C, row * ldc + col, pack_piece<O>(dg), n, whole);
+                    store_piece<O>(C, row * ldc + N + col, pack_piece<O>(du), n, up_whole);
+                } else if constexpr (LIN) {
+#pragma unroll
+                    for (int e = 0; e < VC; ++e)
+                        z[e] += bias[e];
+                    if (ea.Z != nullptr)
+                        store_piece<O>(ea.Z, row * ea.ldz + col, pack_piece<O>(z), n, whole);
+#pragma unroll
+                    for (int e = 0; e < VC; ++e)
+                        z[e] = act_value<KIND>(z[e], ea);
+                    if (R != nullptr)
+#pragma unroll
+                        for (int e = 0; e < VC; ++e)
+                            z[e] += piece_value<O>(r0[t], e);
+                    store_piece<O>(C, row * ldc + col, pack_piece<O>(z), n, whole);
+                } else {
+                    store_piece<O>(C, row * ldc + col, pack_piece<O>(z), n, whole);
+                }
+            }
+        };
+        if constexpr (EPI == EPI_STORE)
+            finish(std::integral_constant<int, AK_CLIP>{});
+        else
+            for_act_kind(ea.kind, finish);
+    };
+    run_pass(std::integral_constant<int, 0>{});
+    if constexpr (WR / PR >= 2)
+        run_pass(std::integral_constant<int, 1>{});
+    if constexpr (WR / PR == 4) {
+        run_pass(std::integral_constant<int, 2>{});
+        run_pass(std::integral_constant<int, 3>{});
+    }
+}
+
 }  // namespace tg

@@ -276,12 +276,23 @@ tg_status glu_typed(const TileArgs& t, const EpiArgs& e, int h_dtype, void* ws, 
 // dW = A^T . B with A stored K x M and B stored K x N (the reduction runs
 // over their rows): the weight gradient, in fp32 or the inputs' type.
 template <int E>
-tg_status wgrad_typed(TileArgs t, int c_dtype, void* ws, int64_t ws_bytes, void* stream)
+tg_status wgrad_typed(const TileArgs& t, int c_dtype, void* ws, int64_t ws_bytes, void* stream)
 {
+    FxArgs a{};
+    static_cast<TileArgs&>(a) = t;
     hipStream_t s = (hipStream_t)stream;
     if (c_dtype == TG_F32)
-        return launch_fused<E, O_F32, B_NCONTIG, EPI_STORE, A_MCONTIG>(t, ws, ws_bytes, s);
-    return launch_fused<E, OutOf<E>::O, B_NCONTIG, EPI_STORE, A_MCONTIG>(t, ws, ws_bytes, s);
+        return launch_fused<E, O_F32, B_NCONTIG, EPI_STORE, A_MCONTIG>(a, ws, ws_bytes, s);
+    return launch_fused<E, OutOf<E>::O, B_NCONTIG, EPI_STORE, A_MCONTIG>(a, ws, ws_bytes, s);
+}
+
+// dX = dZ . W with W as it is stored (row-major in this product)
+template <int E>
+tg_status xgrad_typed(const TileArgs& t, void* ws, int64_t ws_bytes, void* stream)
+{
+    FxArgs a{};
+    static_cast<TileArgs&>(a) = t;
+    return launch_fused<E, OutOf<E>::O, B_NCONTIG, EPI_STORE, A_KCONTIG>(a, ws, ws_bytes, (hipStream_t)stream);
 }
 
 template <int E>

@@ -717,161 +717,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
             x *= p.alpha;
         return x;
     };
+    auto quad = [&](int i, int q) __attribute__((always_inline)) -> f32x4 {
+        const int j = q / 4, v = 4 * (q % 4);
+        return f32x4{out_val(i, j, v), out_val(i, j, v + 1), out_val(i, j, v + 2), out_val(i, j, v + 3)};
+    };
+    (void)quad;
     if constexpr (EPI == EPI_GLU) {
-        // Hidden values are formed in the accumulator layout (a pair of
-        // blocks per output block), rounded to 16 bits, and staged row by row
-        // like a 16-bit output; the kept projections follow in the same LDS.
-        static_assert(O != O_F32, "16-bit hidden values");
-        constexpr int HC = WC / 2;             // hidden columns of this wave
-        constexpr int OB = HC * 2, NCH = OB / 16;
-        static_assert(NW * WR * OB <= LDS_BYTES && WR * NCH % 64 == 0, "epilogue staging");
-        uint8_t* ep = lds + wave * (WR * OB);
-        auto emit = [&](void* dst, int64_t ld, int64_t col0, bool aligned, auto val) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const uint32_t r = i * 32 + lrow;
-#pragma unroll
-                for (int j = 0; j < TN / 2; ++j) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t c = (uint32_t)(4 * j + g);
-                        *(u32x2*)(ep + r * OB + ((c ^ (r % NCH)) << 4) + lgrp * 8) =
-                            u32x2{pack2<O>(val(i, j, 4 * g), val(i, j, 4 * g + 1)),
-                                  pack2<O>(val(i, j, 4 * g + 2), val(i, j, 4 * g + 3))};
-                    }
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
-#pragma unroll
-            for (int t = 0; t < WR * NCH / 64; ++t) {
-                const uint32_t x = t * 64 + lane, r = x / NCH, c = x % NCH;
-                const u32x4 q = lds128(ep, r * OB + ((c ^ (r % NCH)) << 4));
-                const int64_t row = wrow0 + r, col = wcol0 + c * 8, left = N - col;
-                if (row < M && left > 0)
-                    store_piece<O>(dst, row * ld + col0 + col, q, left < 8 ? (int)left : 8, left >= 8 && aligned);
-            }
-        };
-        for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
-            emit(p.C, p.ldc, 0, true, [&](int i, int j, int v) __attribute__((always_inline)) {
-                return act_value<decltype(kind)::value>(out_val(i, 2 * j, v), p.e) * out_val(i, 2 * j + 1, v);
-            });
-        });
-        if (p.e.Z != nullptr) {
-            emit(p.e.Z, p.e.ldz, 0, true,
-                 [&](int i, int j, int v) __attribute__((always_inline)) { return out_val(i, 2 * j, v); });
-            emit(p.e.Z, p.e.ldz, N, N % 8 == 0,
-                 [&](int i, int j, int v) __attribute__((always_inline)) { return out_val(i, 2 * j + 1, v); });
-        }
+        static_assert(NW * WR * WC <= LDS_BYTES, "epilogue staging");
+        glu_epilogue<O, 32, WR, WC>(lds + wave * (WR * WC), lane, wrow0, wcol0, M, N, p.C, p.ldc, p.e, quad);
     } else if constexpr (EPI != EPI_STORE) {
-        // Row-wise epilogues: the fp32 accumulators go through LDS in passes
-        // of PR rows (as an fp32 output does), and come back as pieces of
-        // rows: a lane handles VC consecutive columns, the same ones in every
-        // row, so the bias is loaded once and the other operands are read and
-        // written in 16-byte pieces of whole rows.  A pass's operand loads
-        // are issued ahead of its staging.
-        constexpr int VC = Piece<O>::N;
-        constexpr int LPR = WC / VC, RPT = 64 / LPR;  // lanes per row, rows per instruction
-        constexpr int OB = WC * 4, NCH = OB / 16;
-        constexpr int PBY = LDS_BYTES / NW;
-        constexpr int PR = PBY / OB >= WR ? WR : (PBY / OB >= WR / 2 ? WR / 2 : WR / 4);
-        constexpr int NTI = PR / RPT;
-        constexpr bool BWD = EPI == EPI_GLU_BWD;
-        static_assert(PR % 32 == 0 && WR % PR == 0 && PR % RPT == 0 && 64 % LPR == 0, "staging passes");
-        uint8_t* ep = lds + wave * PBY;
-        const uint32_t ec = lane % LPR, er = lane / LPR;
-        const int64_t col = wcol0 + ec * VC, left = N - col;
-        const int n = left >= VC ? VC : left > 0 ? (int)left : 0;
-        const bool whole = n == VC, up_whole = whole && N % VC == 0;  // (BWD: the up half starts at column N)
-        float bias[VC];
-#pragma unroll
-        for (int e = 0; e < VC; ++e)
-            bias[e] = !BWD && p.e.bias != nullptr && e < n ? p.e.bias[col + e] : 0.0f;
-        // (a call per pass, not a loop: the accumulator must be indexed by constants)
-        auto run_pass = [&](auto pass_c) __attribute__((always_inline)) {
-            constexpr int pass = decltype(pass_c)::value;
-            const int64_t prow = wrow0 + pass * PR + er;
-            u32x4 r0[NTI], r1[BWD ? NTI : 1];
-            if (p.e.R != nullptr) {
-#pragma unroll
-                for (int t = 0; t < NTI; ++t) {
-                    const int64_t row = prow + t * RPT;
-                    r0[t] = u32x4{0u, 0u, 0u, 0u};
-                    if (row < M && n > 0)
-                        r0[t] = load_piece<O>(p.e.R, row * p.e.ldr + col, n, whole);
-                    if constexpr (BWD) {
-                        r1[t] = u32x4{0u, 0u, 0u, 0u};
-                        if (row < M && n > 0)
-                            r1[t] = load_piece<O>(p.e.R, row * p.e.ldr + N + col, n, up_whole);
-                    }
-                }
-            }
-#pragma unroll
-            for (int ii = 0; ii < PR / 32; ++ii) {
-                const int i = pass * (PR / 32) + ii;
-                const uint32_t r = ii * 32 + lrow;
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t c = (uint32_t)(8 * j + 2 * g) + lgrp;
-                        *(f32x4*)(ep + r * OB + ((c ^ (r % NCH)) << 4)) =
-                            f32x4{out_val(i, j, 4 * g), out_val(i, j, 4 * g + 1), out_val(i, j, 4 * g + 2),
-                                  out_val(i, j, 4 * g + 3)};
-                    }
-            }
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
-            for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
-                constexpr int KIND = decltype(kind)::value;
-#pragma unroll
-                for (int t = 0; t < NTI; ++t) {
-                    const uint32_t r = t * RPT + er;
-                    const int64_t row = prow + t * RPT;
-                    float z[VC];
-#pragma unroll
-                    for (int h = 0; h < VC / 4; ++h) {
-                        const f32x4 q = bit_cast<f32x4>(lds128(ep, r * OB + (((ec * (VC / 4) + h) ^ (r % NCH)) << 4)));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            z[4 * h + e] = q[e];
-                    }
-                    if (row >= M || n == 0)
-                        continue;
-                    if constexpr (BWD) {
-                        float dg[VC], du[VC];
-#pragma unroll
-                        for (int e = 0; e < VC; ++e) {
-                            float value;
-                            const float slope = act_slope<KIND>(piece_value<O>(r0[t], e), p.e, value);
-                            dg[e] = z[e] * piece_value<O>(r1[t], e) * slope;
-                            du[e] = z[e] * value;
-                        }
-                        store_piece<O>(p.C, row * p.ldc + col, pack_piece<O>(dg), n, whole);
-                        store_piece<O>(p.C, row * p.ldc + N + col, pack_piece<O>(du), n, up_whole);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VC; ++e)
-                            z[e] += bias[e];
-                        if (p.e.Z != nullptr)
-                            store_piece<O>(p.e.Z, row * p.e.ldz + col, pack_piece<O>(z), n, whole);
-#pragma unroll
-                        for (int e = 0; e < VC; ++e)
-                            z[e] = act_value<KIND>(z[e], p.e);
-                        if (p.e.R != nullptr)
-#pragma unroll
-                            for (int e = 0; e < VC; ++e)
-                                z[e] += piece_value<O>(r0[t], e);
-                        store_piece<O>(p.C, row * p.ldc + col, pack_piece<O>(z), n, whole);
-                    }
-                }
-            });
-        };
-        run_pass(std::integral_constant<int, 0>{});
-        if constexpr (WR / PR >= 2)
-            run_pass(std::integral_constant<int, 1>{});
-        if constexpr (WR / PR == 4) {
-            run_pass(std::integral_constant<int, 2>{});
-            run_pass(std::integral_constant<int, 3>{});
-        }
+        rows_epilogue<O, EPI, 32, WR, WC, LDS_BYTES / NW>(lds + wave * (LDS_BYTES / NW), lane, wrow0, wcol0, M, N, p.C, p.ldc,
+                                                          p.e, quad);
     } else if constexpr (O == O_F32) {
         // fp32 output: staged through LDS like the 16-bit one, so that the
         // stores are whole rows (a lane's 4 columns stored directly give 32

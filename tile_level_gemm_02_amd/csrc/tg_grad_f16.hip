@@ -7,6 +7,11 @@ tg_status wgrad_f16(const TileArgs& t, int c_dtype, void* ws, int64_t ws_bytes, 
     return wgrad_typed<E_F16>(t, c_dtype, ws, ws_bytes, stream);
 }
 
+tg_status xgrad_f16(const TileArgs& t, void* ws, int64_t ws_bytes, void* stream)
+{
+    return xgrad_typed<E_F16>(t, ws, ws_bytes, stream);
+}
+
 tg_status glu_dgu_f16(const TileArgs& t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream)
 {
     return glu_dgu_typed<E_F16>(t, e, ws, ws_bytes, stream);

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "tg_abi.hpp"
+#include "tg_gemm_fx.hpp"
 #include "tg_gemm_nt.hpp"
 #include "tg_gemm_skinny.hpp"
 #include "tg_kernels.hpp"
@@ -364,7 +365,8 @@ NtPlan plan_nt(int64_t M, int64_t N, int64_t K, bool allow_split)
     return p;
 }
 
-// (EPI, AL, P: a fused epilogue and a transposed A, see gemm_nt.  EPI_GLU
+// (EPI, AL, P: a fused epilogue and a transposed A, see gemm_nt; the 256 tile
+// of such products with 16-bit inputs is gemm_fx's.  EPI_GLU
 // stages 2 N columns; its 64 tile runs 2 waves of 32 x 64, so that each wave
 // holds a gate block and the up block beside it.)
 template <int E, int O, int BM, int BN, int BL, int NH, int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
@@ -376,6 +378,10 @@ tg_status launch_nt(const P& a, int splits, hipStream_t s, int64_t grid_override
         return TG_ERR_NOT_SUPPORTED;
     constexpr int RB = NtStaging<E>::RB;
     constexpr int WM = NtWaves<E, BM, BN>::WM, WN = EPI == EPI_GLU && BN == 64 ? 1 : NtWaves<E, BM, BN>::WN;
+    if constexpr (!std::is_same<P, TileArgs>::value && ElemInfo<E>::bytes == 2 && BM == 256 && BN == 256) {
+        hipLaunchKernelGGL((gemm_fx<E, O, NH, AL, BL, EPI, P>), dim3((uint32_t)grid), dim3(512), 0, s, a);
+        return launched();
+    }
     hipLaunchKernelGGL((gemm_nt<E, O, BM, BN, RB, NH, WM, WN, BL, EPI, AL, P>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, s, a);
     return launched();
 }

@@ -17,6 +17,8 @@ tg_status wgrad_f16(Prod t, int c_dtype, void* ws, int64_t ws_bytes, void* strea
 tg_status wgrad_bf16(Prod t, int c_dtype, void* ws, int64_t ws_bytes, void* stream);
 int64_t wgrad_ws_bytes_f16(int64_t N, int64_t K, int64_t M);
 int64_t wgrad_ws_bytes_bf16(int64_t N, int64_t K, int64_t M);
+tg_status xgrad_f16(Prod t, void* ws, int64_t ws_bytes, void* stream);
+tg_status xgrad_bf16(Prod t, void* ws, int64_t ws_bytes, void* stream);
 tg_status glu_dgu_f16(Prod t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream);
 tg_status glu_dgu_bf16(Prod t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream);
 tg_status dz_f16(const DzArgs& p, void* ws, int64_t ws_bytes, void* stream);
@@ -62,13 +64,13 @@ static int64_t glu_bwd_ws(int in, int64_t M, int64_t F, int64_t D)
                   larger(wgrad_ws(in, 2 * F, D, M), wgrad_ws(in, D, F, M)));
 }
 
-// C (M x N) = A . B with B row-major, on the plain GEMM's path
+// C (M x N) = A . B with B row-major
 static tg_status product_row(int in, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                              int64_t ldb, void* C, int64_t ldc, void* ws, int64_t ws_bytes, void* stream)
 {
-    if (in == TG_IN_F16)
-        return gemm_f16_ws(M, N, K, A, lda, B, ldb, TG_ROW_MAJOR, C, ldc, TG_F16, stream, ws, ws_bytes);
-    return gemm_bf16_ws(M, N, K, A, lda, B, ldb, TG_ROW_MAJOR, C, ldc, TG_BF16, stream, ws, ws_bytes);
+    TileArgs t{};
+    set_product(t, M, N, K, A, lda, B, ldb, C, ldc, 1.0f);
+    return in == TG_IN_F16 ? xgrad_f16(t, ws, ws_bytes, stream) : xgrad_bf16(t, ws, ws_bytes, stream);
 }
 
 // C (M x N) = A^T . B with A stored K x M and B stored K x N

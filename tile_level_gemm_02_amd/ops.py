@@ -64,6 +64,10 @@ def _lib():
 
 
 # ------------------------------------------------------------- marshalling
+#
+# A small product's kernel runs in 5 to 10 us, so a call's marshalling is kept
+# near that: each tensor attribute is read once (about 0.1 us each), and the
+# current device and stream are read without torch.cuda's wrappers.
 
 
 def _act(name: str) -> int:
@@ -73,56 +77,58 @@ def _act(name: str) -> int:
         raise ValueError(f"unknown activation {name!r}: one of {', '.join(ACTS)}") from None
 
 
-def _mat(t, name: str, rows: int, cols: int, dtypes):
-    """(pointer, leading dimension) of a rows x cols matrix of one of `dtypes`."""
+def _mat(t, name: str, rows: int, cols: int, dtypes, dev: int):
+    """(pointer, leading dimension) of a rows x cols matrix of one of `dtypes` on GPU `dev`."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows}x{cols}, got shape {tuple(t.shape)}")
-    s = t.stride()
-    if cols > 1 and s[1] != 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.data_ptr(), (s[0] if rows > 1 else max(s[0], cols))
+    if t.get_device() != dev:
+        raise ValueError(f"every tensor must be on the current GPU, {name} is on {t.device}")
+    return t.data_ptr(), (ld if rows > 1 or ld > cols else cols)
 
 
-def _opt(t, name: str, rows: int, cols: int, dtypes):
-    return (None, 0) if t is None else _mat(t, name, rows, cols, dtypes)
+_NONE = (None, 0)
 
 
 def _2d(t, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    return shape
 
 
-def _vec(t, name: str, n: int):
-    if t is None:
-        return None
+def _vec(t, name: str, n: int, dev: int):
     if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 vector of {n}")
+    if t.get_device() != dev:
+        raise ValueError(f"every tensor must be on the current GPU, {name} is on {t.device}")
     return t.data_ptr()
 
 
-def _ws(workspace):
+def _ws(workspace, dev: int):
     if workspace is None:
-        return None, 0
+        return _NONE
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev:
+        raise ValueError(f"every tensor must be on the current GPU, the workspace is on {workspace.device}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
-def _on_device(*tensors) -> None:
-    """Every tensor given is on the current GPU."""
-    want = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    for t in tensors:
-        if t is not None and t.get_device() != want:
-            raise ValueError(f"every tensor must be on the current GPU, got one on {t.device}")
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(name: str, *args) -> None:
-    code = getattr(_fns, name)(*args)
-    if code:
-        raise TGError(name, code)
+def _device(t, name: str) -> int:
+    """The index of the current GPU, which `t` has to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"every tensor must be on the current GPU, {name} is on {t.device}")
+    return dev
 
 
 def _input(x, what: str) -> int:
@@ -133,9 +139,15 @@ def _input(x, what: str) -> int:
 
 
 def _input16(x, what: str) -> int:
-    if x.dtype not in (torch.float16, torch.bfloat16):
+    if x.dtype not in _16BIT:
         raise ValueError(f"{what} takes float16 or bfloat16 inputs, got {x.dtype}")
     return _IN[x.dtype]
+
+
+_16BIT = (torch.float16, torch.bfloat16)
+_OWN = {d: (d,) for d in (*_CDTYPE, *_IN)}
+_OWN_OR_F32 = {d: (torch.float32, d) for d in _16BIT}
+_OWN_OR_F32[torch.float8_e4m3fn] = tuple(_CDTYPE)
 
 
 def _bytes(name: str, dtype, *sizes: int) -> int:
@@ -178,23 +190,24 @@ def tg_ops_workspace(device="cuda"):
 def tg_linear(x, W, Y, bias=None, act: str = "none", residual=None, preact=None, scale_x: float = 1.0,
               scale_w: float = 1.0, workspace=None, stream=None) -> None:
     """Y = act(z) + residual, z = scale_x scale_w x . W^T + bias; z is kept in ``preact`` if given."""
-    _lib()
     i = _input(x, "tg_linear")
     M, K = _2d(x, "x")
-    N = _2d(W, "W")[0]
+    N = W.shape[0]
     a = _act(act)
-    own = (x.dtype,)
-    px, ldx = _mat(x, "x", M, K, own)
-    pw, ldw = _mat(W, "W", N, K, own)
-    out = _CDTYPE if i == 2 else (torch.float32, x.dtype)
-    py, ldy = _mat(Y, "Y", M, N, out)
-    like = (Y.dtype,)
-    pr, ldr = _opt(residual, "residual", M, N, like)
-    pz, ldz = _opt(preact, "preact", M, N, like)
-    pb = _vec(bias, "bias", N)
-    _on_device(x, W, Y, bias, residual, preact, workspace)
-    _call("tg_linear", i, M, N, K, px, ldx, pw, ldw, pb, a, pr, ldr, scale_x, scale_w, py, ldy, _CDTYPE[Y.dtype], pz, ldz,
-          *_ws(workspace), _stream(stream))
+    dev = _device(x, "x")
+    own = _OWN[x.dtype]
+    px, ldx = _mat(x, "x", M, K, own, dev)
+    pw, ldw = _mat(W, "W", N, K, own, dev)
+    py, ldy = _mat(Y, "Y", M, N, _OWN_OR_F32[x.dtype], dev)
+    yt = Y.dtype
+    pr, ldr = _NONE if residual is None else _mat(residual, "residual", M, N, _OWN[yt], dev)
+    pz, ldz = _NONE if preact is None else _mat(preact, "preact", M, N, _OWN[yt], dev)
+    pb = None if bias is None else _vec(bias, "bias", N, dev)
+    ps, ns = _ws(workspace, dev)
+    code = (_fns or _lib()).tg_linear(i, M, N, K, px, ldx, pw, ldw, pb, a, pr, ldr, scale_x, scale_w, py, ldy, _CDTYPE[yt],
+                                      pz, ldz, ps, ns, _current_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise TGError("tg_linear", code)
 
 
 def tg_linear_backward(dY, x, W, dx=None, dw=None, dbias=None, preact=None, act: str = "none", dz=None, workspace=None,
@@ -204,45 +217,52 @@ def tg_linear_backward(dY, x, W, dx=None, dw=None, dbias=None, preact=None, act:
     Each output that is given is written.  With an activation ``dz`` is a
     buffer like dY (dY itself may serve); without one dz is dY, and
     ``preact`` and ``dz`` are not looked at."""
-    _lib()
     i = _input16(dY, "tg_linear_backward")
     M, N = _2d(dY, "dY")
     K = _2d(x, "x")[1]
     a = _act(act)
-    own = (dY.dtype,)
-    pd, ldd = _mat(dY, "dY", M, N, own)
-    px, ldx = _mat(x, "x", M, K, own)
-    pw, ldw = _mat(W, "W", N, K, own)
     if a == 0:
         preact = dz = None
     elif preact is None or dz is None:
         raise ValueError("an activation's gradient needs preact and a dz buffer")
-    pz, ldz = _opt(preact, "preact", M, N, own)
-    pq, ldq = _opt(dz, "dz", M, N, own)
-    pdx, lddx = _opt(dx, "dx", M, K, own)
-    pdw, lddw = _opt(dw, "dw", N, K, (torch.float32, dY.dtype))
-    pb = _vec(dbias, "dbias", N)
-    _on_device(dY, x, W, preact, dz, dx, dw, dbias, workspace)
-    _call("tg_linear_backward", i, M, N, K, pd, ldd, px, ldx, pw, ldw, pz, ldz, a, pq, ldq, pdx, lddx, pdw, lddw,
-          0 if dw is None else _CDTYPE[dw.dtype], pb, *_ws(workspace), _stream(stream))
+    dev = _device(dY, "dY")
+    t = dY.dtype
+    own = _OWN[t]
+    pd, ldd = _mat(dY, "dY", M, N, own, dev)
+    px, ldx = _mat(x, "x", M, K, own, dev)
+    pw, ldw = _mat(W, "W", N, K, own, dev)
+    pz, ldz = _NONE if preact is None else _mat(preact, "preact", M, N, own, dev)
+    pq, ldq = _NONE if dz is None else _mat(dz, "dz", M, N, own, dev)
+    pdx, lddx = _NONE if dx is None else _mat(dx, "dx", M, K, own, dev)
+    pdw, lddw = _NONE if dw is None else _mat(dw, "dw", N, K, _OWN_OR_F32[t], dev)
+    pb = None if dbias is None else _vec(dbias, "dbias", N, dev)
+    ps, ns = _ws(workspace, dev)
+    code = (_fns or _lib()).tg_linear_backward(
+        i, M, N, K, pd, ldd, px, ldx, pw, ldw, pz, ldz, a, pq, ldq, pdx, lddx, pdw, lddw,
+        0 if dw is None else _CDTYPE[dw.dtype], pb, ps, ns, _current_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise TGError("tg_linear_backward", code)
 
 
 def tg_glu(x, W, H, act: str = "silu", gate_up=None, scale_x: float = 1.0, scale_w: float = 1.0, workspace=None,
            stream=None) -> None:
     """H = act(g) * u with [g | u] = scale_x scale_w x . W^T, W = [Wg; Wu] (2F x D); [g | u] is kept in ``gate_up`` if given."""
-    _lib()
     i = _input(x, "tg_glu")
     M, D = _2d(x, "x")
     F = _2d(H, "H")[1]
     a = _act(act)
-    own = (x.dtype,)
-    px, ldx = _mat(x, "x", M, D, own)
-    pw, ldw = _mat(W, "W", 2 * F, D, own)
-    ph, ldh = _mat(H, "H", M, F, (torch.float16, torch.bfloat16) if i == 2 else own)
-    pg, ldg = _opt(gate_up, "gate_up", M, 2 * F, (H.dtype,))
-    _on_device(x, W, H, gate_up, workspace)
-    _call("tg_glu", i, M, F, D, px, ldx, pw, ldw, a, scale_x, scale_w, ph, ldh, _CDTYPE[H.dtype], pg, ldg,
-          *_ws(workspace), _stream(stream))
+    dev = _device(x, "x")
+    own = _OWN[x.dtype]
+    px, ldx = _mat(x, "x", M, D, own, dev)
+    pw, ldw = _mat(W, "W", 2 * F, D, own, dev)
+    ph, ldh = _mat(H, "H", M, F, _16BIT if i == 2 else own, dev)
+    ht = H.dtype
+    pg, ldg = _NONE if gate_up is None else _mat(gate_up, "gate_up", M, 2 * F, _OWN[ht], dev)
+    ps, ns = _ws(workspace, dev)
+    code = (_fns or _lib()).tg_glu(i, M, F, D, px, ldx, pw, ldw, a, scale_x, scale_w, ph, ldh, _CDTYPE[ht], pg, ldg, ps, ns,
+                                   _current_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise TGError("tg_glu", code)
 
 
 def tg_glu_backward(dY, Wd, x, W, gate_up, H, dgate_up, dx=None, dw_gate_up=None, dw_down=None, act: str = "silu",
@@ -252,30 +272,34 @@ def tg_glu_backward(dY, Wd, x, W, gate_up, H, dgate_up, dx=None, dw_gate_up=None
     ``dgate_up`` (M x 2F, may be gate_up itself) receives [dg | du]; each of
     dx, dw_gate_up (2F x D) and dw_down (D x F) that is given is written.
     ``H`` may be None where dw_down is."""
-    _lib()
     i = _input16(dY, "tg_glu_backward")
     M, D = _2d(dY, "dY")
     F = _2d(Wd, "Wd")[1]
     a = _act(act)
-    own = (dY.dtype,)
-    args = []
-    for t, name, rows, cols in ((dY, "dY", M, D), (Wd, "Wd", D, F), (x, "x", M, D), (W, "W", 2 * F, D),
-                                (gate_up, "gate_up", M, 2 * F)):
-        args += _mat(t, name, rows, cols, own)
     if H is None and dw_down is not None:
         raise ValueError("dw_down needs H")
-    args += _opt(H, "H", M, F, own)
-    args.append(a)
-    args += _mat(dgate_up, "dgate_up", M, 2 * F, own)
-    args += _opt(dx, "dx", M, D, own)
-    out = (torch.float32, dY.dtype)
-    args += _opt(dw_gate_up, "dw_gate_up", 2 * F, D, out)
-    args += _opt(dw_down, "dw_down", D, F, out)
-    given = {t.dtype for t in (dw_gate_up, dw_down) if t is not None}
-    if len(given) > 1:
+    if dw_gate_up is not None and dw_down is not None and dw_gate_up.dtype != dw_down.dtype:
         raise ValueError("dw_gate_up and dw_down must have one type")
-    _on_device(dY, Wd, x, W, gate_up, H, dgate_up, dx, dw_gate_up, dw_down, workspace)
-    _call("tg_glu_backward", i, M, F, D, *args, _CDTYPE[given.pop()] if given else 0, *_ws(workspace), _stream(stream))
+    dev = _device(dY, "dY")
+    t = dY.dtype
+    own, out = _OWN[t], _OWN_OR_F32[t]
+    pd, ldd = _mat(dY, "dY", M, D, own, dev)
+    pwd, ldwd = _mat(Wd, "Wd", D, F, own, dev)
+    px, ldx = _mat(x, "x", M, D, own, dev)
+    pw, ldw = _mat(W, "W", 2 * F, D, own, dev)
+    pg, ldg = _mat(gate_up, "gate_up", M, 2 * F, own, dev)
+    ph, ldh = _NONE if H is None else _mat(H, "H", M, F, own, dev)
+    pq, ldq = _mat(dgate_up, "dgate_up", M, 2 * F, own, dev)
+    pdx, lddx = _NONE if dx is None else _mat(dx, "dx", M, D, own, dev)
+    pdw, lddw = _NONE if dw_gate_up is None else _mat(dw_gate_up, "dw_gate_up", 2 * F, D, out, dev)
+    pdd, lddd = _NONE if dw_down is None else _mat(dw_down, "dw_down", D, F, out, dev)
+    ps, ns = _ws(workspace, dev)
+    wt = dw_gate_up if dw_gate_up is not None else dw_down
+    code = (_fns or _lib()).tg_glu_backward(
+        i, M, F, D, pd, ldd, pwd, ldwd, px, ldx, pw, ldw, pg, ldg, ph, ldh, a, pq, ldq, pdx, lddx, pdw, lddw, pdd, lddd,
+        0 if wt is None else _CDTYPE[wt.dtype], ps, ns, _current_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise TGError("tg_glu_backward", code)
 
 
 # ---------------------------------------------------------------- clipping
@@ -295,32 +319,37 @@ def tg_clip_grads(grads, max_norm: float, out=None, norm=None, eps: float = 1e-6
     ``out`` None clips in place; ``norm`` (float32, one element) receives the
     norm before clipping.  Tensors are contiguous, of float32, float16 or
     bfloat16, mixed as they come.  Nothing is copied to the host."""
-    _lib()
     grads = list(grads)
     count = len(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != count:
-        raise ValueError(f"out must hold {count} tensors, got {len(outs)}")
+    if workspace is None:
+        raise ValueError("tg_clip_grads needs a workspace")
     try:
         types = array.array("i", [_CDTYPE[g.dtype] for g in grads])
     except KeyError as e:
         raise ValueError(f"unsupported gradient dtype {e.args[0]}") from None
+    if out is None:
+        outs = grads
+    else:
+        outs = list(out)
+        if [(o.dtype, o.shape) for o in outs] != [(g.dtype, g.shape) for g in grads]:
+            raise ValueError(f"out must hold {count} tensors like the gradients")
+    every = grads if out is None else grads + outs
+    if not all([t.is_contiguous() for t in every]):
+        raise ValueError("gradients and outputs must be contiguous")
+    if norm is not None:
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be a float32 tensor of one element")
+        every = every + [norm]
+    dev = _device(workspace, "the workspace")
+    if any([t.get_device() != dev for t in every]):
+        raise ValueError("every tensor must be on the current GPU")
+    ps, ns = _ws(workspace, dev)
+    # host arrays of pointers, sizes and types: one buffer of pointers for both sides
+    ptrs = array.array("Q", [t.data_ptr() for t in every])
     sizes = array.array("q", [g.numel() for g in grads])
-    pin = array.array("Q", [g.data_ptr() for g in grads])
-    pout = pin
-    for g in grads:
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-    if out is not None:
-        for g, o in zip(grads, outs):
-            if o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
-                raise ValueError("each out must be a contiguous tensor like its gradient")
-        pout = array.array("Q", [o.data_ptr() for o in outs])
-    if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1):
-        raise ValueError("norm must be a float32 tensor of one element")
-    if workspace is None:
-        raise ValueError("tg_clip_grads needs a workspace")
-    _on_device(workspace, norm, *grads, *(outs if out is not None else ()))
-    _call("tg_clip_grads", count, pin.buffer_info()[0], pout.buffer_info()[0], sizes.buffer_info()[0],
-          types.buffer_info()[0], max_norm, eps, None if norm is None else norm.data_ptr(), *_ws(workspace),
-          _stream(stream))
+    pin = ptrs.buffer_info()[0]
+    code = (_fns or _lib()).tg_clip_grads(
+        count, pin, pin if out is None else pin + 8 * count, sizes.buffer_info()[0], types.buffer_info()[0], max_norm, eps,
+        None if norm is None else ptrs[-1], ps, ns, _current_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise TGError("tg_clip_grads", code)
