@@ -379,11 +379,16 @@ tg_status launch_nt(const P& a, int splits, hipStream_t s, int64_t grid_override
     constexpr int RB = NtStaging<E>::RB;
     constexpr int WM = NtWaves<E, BM, BN>::WM, WN = EPI == EPI_GLU && BN == 64 ? 1 : NtWaves<E, BM, BN>::WN;
     if constexpr (!std::is_same<P, TileArgs>::value && ElemInfo<E>::bytes == 2 && BM == 256 && BN == 256) {
-        hipLaunchKernelGGL((gemm_fx<E, O, NH, AL, BL, EPI, P>), dim3((uint32_t)grid), dim3(512), 0, s, a);
+        // (five ring slots, four with both operands as k rows, whose moving
+        // bases leave no registers for the addresses of five: 40 spills)
+        constexpr int FNH = AL == A_MCONTIG ? 4 : 5;
+        hipLaunchKernelGGL((gemm_fx<E, O, FNH, AL, BL, EPI, P>), dim3((uint32_t)grid), dim3(512), 0, s, a);
+        return launched();
+    } else {
+        hipLaunchKernelGGL((gemm_nt<E, O, BM, BN, RB, NH, WM, WN, BL, EPI, AL, P>), dim3((uint32_t)grid),
+                           dim3(64 * WM * WN), 0, s, a);
         return launched();
     }
-    hipLaunchKernelGGL((gemm_nt<E, O, BM, BN, RB, NH, WM, WN, BL, EPI, AL, P>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, s, a);
-    return launched();
 }
 
 // Launch an NT plan.  With plan.splits > 1, `ws` is a zeroed-counter
