@@ -323,7 +323,7 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
 #pragma unroll
         for (int b = 0; b < 32; ++b)
             splitk_store(slot(ks), b / 4, b % 4, lane, acc[b / 4][b % 4]);
-        if (!splitk_last(p.counters + (size_t)stile * NW + wave, S, lane))
+        if (!splitk_last(p.counters + ((size_t)stile * NW + wave) * kCounterStride<P, TileArgs>, S, lane))
             return;
         for (uint32_t q = ks == 0u ? 1u : 0u; q < S; ++q) {
             const float* src = slot(q);

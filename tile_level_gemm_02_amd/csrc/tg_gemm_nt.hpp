@@ -633,7 +633,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
                 for (int g = 0; g < 4; ++g)
                     splitk_store(slot(ks), i * TN + j, g, lane,
                                  f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
-        if (!splitk_last(p.counters + (size_t)tile * NW + wave, S, lane))
+        if (!splitk_last(p.counters + ((size_t)tile * NW + wave) * kCounterStride<P, TileArgs>, S, lane))
             return;
         // the S partial shares in split order: acc = p_0, then acc += p_q
         // for q = 1 .. S-1.  Up to 4 accumulator blocks per wave (the 64 and

@@ -245,7 +245,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
 #pragma unroll
                 for (int q = 0; q < NG; ++q)
                     splitk_store(slot0 + me * (NG * 256), 0, q, lane, sum[q]);
-                if (!splitk_last(p.counters + id, S, lane))
+                if (!splitk_last(p.counters + id * kCounterStride<P, SkinnyArgs>, S, lane))
                     return;
                 f32x4 own[NG];
 #pragma unroll

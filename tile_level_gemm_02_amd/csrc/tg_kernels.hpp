@@ -55,6 +55,15 @@ struct FusedArgs : TileArgs {
     EpiArgs e;
 };
 
+// Words between the arrival counters of a K split.  The feed-forward
+// operators' calls give each counter a 64-byte line: arrivals at one line
+// queue up at the device-coherent level (1024 arrivals at 16 counters of one
+// line took 14 us).  A split's workgroups fit one round of the chip, so their
+// counters fit the workspace's 64 KiB: at most 128 tiles of 4 waves, or 128
+// last-round tiles of 8.
+template <class P, class Plain>
+constexpr uint32_t kCounterStride = std::is_same<P, Plain>::value ? 1u : 16u;
+
 // B storage: K-contiguous (column-major K x N, i.e. N x K rows) or N-contiguous
 enum BLay : int { B_KCONTIG = 0, B_NCONTIG = 1 };
 // A storage: K-contiguous (M x K rows) or M-contiguous (the transpose: K x M rows)
