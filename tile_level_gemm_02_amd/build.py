@@ -1,4 +1,5 @@
-"""Build libtg.so (the HIP kernels + C ABI) in-tree with hipcc for gfx950.
+"""Build libtg.so (the HIP kernels + C ABI) in-tree with hipcc for gfx950, and
+the Python binding's native helper _tgbind.so with g++.
 
     python -m tile_level_gemm_02_amd.build          # or build() from Python
 
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtg.so")
+BIND = os.path.join(PKG, "_tgbind.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 ARCH = "gfx950"
@@ -42,14 +44,36 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_bind() -> None:
+    """csrc/bind.cpp against torch's C++ headers (no GPU code)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *cpp_extension.include_paths()]
+    libs = cpp_extension.library_paths()
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in inc), os.path.join(CSRC, "bind.cpp"),
+           *(f"-L{d}" for d in libs), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(extra: list[str] | None = None, jobs: int | None = None) -> str:
-    """Compile every HIP source and link libtg.so; returns its path."""
+    """Compile every HIP source, link libtg.so and compile _tgbind.so; returns libtg.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     extra = list(extra or [])
     jobs = jobs or min(len(srcs), max(1, (os.cpu_count() or 2)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        bind.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

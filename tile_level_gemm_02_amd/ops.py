@@ -16,8 +16,10 @@ anything is launched, what the library itself refuses raises TGError.
 """
 from __future__ import annotations
 
-import array
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
@@ -34,11 +36,23 @@ EXPORTS = ("tg_linear", "tg_linear_workspace_bytes", "tg_linear_backward", "tg_l
 WORKSPACE_BYTES = (64 << 20) + (64 << 10)
 
 _fns = None
+_bind = None          # the native helper _tgbind.so
+_clip_address = 0     # of tg_clip_grads in the loaded library
+_BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tgbind.so")
+
+
+def _load_bind():
+    if not os.path.exists(_BIND_PATH):
+        raise ImportError(f"{_BIND_PATH} is not built; run `python -m tile_level_gemm_02_amd.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_tgbind", _BIND_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tgbind", loader))
+    loader.exec_module(module)
+    return module
 
 
 def _lib():
     """The library with the argument types of these entry points set."""
-    global _fns
+    global _fns, _bind, _clip_address
     if _fns is None:
         lib = load()
         i64, vp, f32, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int
@@ -59,6 +73,8 @@ def _lib():
             fn.argtypes, fn.restype = [ci, i64, i64, i64], i64
         lib.tg_clip_grads_workspace_bytes.argtypes = [i64]
         lib.tg_clip_grads_workspace_bytes.restype = i64
+        _bind = _load_bind()
+        _clip_address = ctypes.cast(lib.tg_clip_grads, ctypes.c_void_p).value
         _fns = lib
     return _fns
 
@@ -319,37 +335,14 @@ def tg_clip_grads(grads, max_norm: float, out=None, norm=None, eps: float = 1e-6
     ``out`` None clips in place; ``norm`` (float32, one element) receives the
     norm before clipping.  Tensors are contiguous, of float32, float16 or
     bfloat16, mixed as they come.  Nothing is copied to the host."""
-    grads = list(grads)
-    count = len(grads)
     if workspace is None:
         raise ValueError("tg_clip_grads needs a workspace")
-    try:
-        types = array.array("i", [_CDTYPE[g.dtype] for g in grads])
-    except KeyError as e:
-        raise ValueError(f"unsupported gradient dtype {e.args[0]}") from None
-    if out is None:
-        outs = grads
-    else:
-        outs = list(out)
-        if [(o.dtype, o.shape) for o in outs] != [(g.dtype, g.shape) for g in grads]:
-            raise ValueError(f"out must hold {count} tensors like the gradients")
-    every = grads if out is None else grads + outs
-    if not all([t.is_contiguous() for t in every]):
-        raise ValueError("gradients and outputs must be contiguous")
-    if norm is not None:
-        if norm.dtype != torch.float32 or norm.numel() != 1:
-            raise ValueError("norm must be a float32 tensor of one element")
-        every = every + [norm]
     dev = _device(workspace, "the workspace")
-    if any([t.get_device() != dev for t in every]):
-        raise ValueError("every tensor must be on the current GPU")
     ps, ns = _ws(workspace, dev)
-    # host arrays of pointers, sizes and types: one buffer of pointers for both sides
-    ptrs = array.array("Q", [t.data_ptr() for t in every])
-    sizes = array.array("q", [g.numel() for g in grads])
-    pin = ptrs.buffer_info()[0]
-    code = (_fns or _lib()).tg_clip_grads(
-        count, pin, pin if out is None else pin + 8 * count, sizes.buffer_info()[0], types.buffer_info()[0], max_norm, eps,
-        None if norm is None else ptrs[-1], ps, ns, _current_stream(dev) if stream is None else _stream(stream))
+    if _fns is None:
+        _lib()
+    code = _bind.clip_grads(_clip_address, grads if type(grads) is list else list(grads),
+                            out if out is None or type(out) is list else list(out), max_norm, eps, norm, dev, ps, ns,
+                            _current_stream(dev) if stream is None else _stream(stream))
     if code:
         raise TGError("tg_clip_grads", code)
