@@ -46,7 +46,6 @@ struct ClipArgs {
     double* partials;
     float* norm;
     float max_norm, eps;
-    int32_t stream;                   // the scaling reads with the non-temporal hint
 };
 
 __device__ __forceinline__ int tensor_of_chunk(const ClipArgs& p, uint32_t c)
@@ -165,13 +164,16 @@ __global__ __launch_bounds__(256) void clip_sum(ClipArgs p)
     }
 }
 
+// STREAM: the gradients are read with the non-temporal hint (a template
+// parameter: the compiler folds a branch between the two loads into one
+// without the hint)
+template <bool STREAM>
 __global__ __launch_bounds__(256) void clip_scale(ClipArgs p)
 {
     const double d = __builtin_sqrt(*p.total) + (double)p.eps;
     const double c = d == 0.0 ? 1.0 : (double)p.max_norm / d;
     const float coef = c > 1.0 ? 1.0f : (float)c;  // (NaN stays)
     const uint32_t chunks = p.first[p.count];
-    const bool stream = p.stream != 0;
     for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
         const uint32_t ch = chunks - 1u - i;
         const int t = tensor_of_chunk(p, ch);
@@ -186,7 +188,11 @@ __global__ __launch_bounds__(256) void clip_scale(ClipArgs p)
             over_chunk<O, decltype(whole)::value>(e0, n, [&](auto piece, int64_t e) __attribute__((always_inline)) {
                 if constexpr (decltype(piece)::value) {
                     const u32x4* src = (const u32x4*)((const typename OutInfo<O>::T*)g + e);
-                    const u32x4 q = stream ? __builtin_nontemporal_load(src) : *src;
+                    u32x4 q;
+                    if constexpr (STREAM)
+                        q = __builtin_nontemporal_load(src);
+                    else
+                        q = *src;
                     float v[Piece<O>::N];
 #pragma unroll
                     for (int j = 0; j < Piece<O>::N; ++j)
@@ -260,7 +266,6 @@ extern "C" tg_status tg_clip_grads(int64_t count, const void* const* grads, void
     p.norm = norm;
     p.max_norm = max_norm;
     p.eps = eps;
-    p.stream = bytes > (int64_t)256 << 20;
     // fill the descriptors from tensor i on; returns the next tensor
     auto fill = [&](int64_t i, int64_t* grid) -> int64_t {
         int64_t chunks = 0;
@@ -307,7 +312,10 @@ extern "C" tg_status tg_clip_grads(int64_t count, const void* const* grads, void
         i = fill(i, &grid);
         if (p.count == 0)
             continue;
-        hipLaunchKernelGGL(clip_scale, dim3((uint32_t)grid), dim3(256), 0, s, p);
+        if (bytes > (int64_t)256 << 20)
+            hipLaunchKernelGGL(clip_scale<true>, dim3((uint32_t)grid), dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL(clip_scale<false>, dim3((uint32_t)grid), dim3(256), 0, s, p);
         if (hipGetLastError() != hipSuccess)
             return TG_ERR_LAUNCH;
     }
