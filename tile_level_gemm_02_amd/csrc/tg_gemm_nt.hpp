@@ -129,12 +129,20 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// WM x WN waves share the tile (each computes a BM/WM x BN/WN sub-tile).
+// LDS of a tile's ring
+template <int BM, int BN, int RB, int NH>
+constexpr int nt_lds_bytes()
+{
+    return NH % 2 == 0 ? NH / 2 * (BM + BN) * RB : NH * (BM > BN ? BM : BN) * RB;
+}
+
+// The kernel's body, for workgroup `bid` of `nblocks`, with the ring at `lds`
+// (1 KiB aligned).  WM x WN waves share the tile (each computes a BM/WM x BN/WN sub-tile).
 // With 8 waves (two per SIMD) the LDS sustains about twice the fragment-read
 // rate of 4 waves (one per SIMD), which the 256 x 256 tile needs.
 template <int E, int O, int BM, int BN, int RB, int NH, int WM = 2, int WN = 2, int BL = B_KCONTIG,
           int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
+__device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t nblocks, uint8_t* lds)
 {
     constexpr bool GLU = EPI == EPI_GLU;
     constexpr int BNO = GLU ? BN / 2 : BN;  // output columns per tile
@@ -157,7 +165,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
     // every slot takes the larger size.
     constexpr int ASZ = BM * RB, BSZ = BN * RB;
     constexpr int HALF = (BM > BN ? BM : BN) * RB;
-    constexpr int LDS_BYTES = NH % 2 == 0 ? NH / 2 * (ASZ + BSZ) : NH * HALF;
+    constexpr int LDS_BYTES = nt_lds_bytes<BM, BN, RB, NH>();
     static_assert(NH % 2 == 0 || BM == BN, "odd ring depths take square tiles");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
     // byte offset of half-stage h's slot
@@ -218,8 +226,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
     static_assert(!GLU || (BL == B_KCONTIG && TN % 2 == 0 && RPI == 8 && (BN / NW == 32 || BN / NW == 64)),
                   "gate and up blocks side by side in a wave");
 
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
-
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform: keeps LDS bases scalar
     const int64_t M = p.M, N = p.N, K = p.K;
@@ -241,7 +247,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
         constexpr uint32_t QM = 256 / BM, QN = 256 / BN, Q = QM * QN;
         static_assert(QM * BM == 256 && QN * BN == 256, "parts of a 256 x 256 tile");
         const uint32_t tm2 = (uint32_t)((M + 255) / 256), tn2 = (uint32_t)(GLU ? (N + 127) / 128 : (N + 255) / 256);
-        const uint32_t j = xcd_remap(blockIdx.x, gridDim.x);
+        const uint32_t j = xcd_remap(bid, nblocks);
         uint32_t t_m, t_n;
         group_walk(p.sub256 - 1u + j / Q, tm2, tn2, p.group_m, t_m, t_n);
         tmi = t_m * QM + (j % Q) / QN;
@@ -250,15 +256,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
         if ((int64_t)tmi * BM >= M || (int64_t)tni * BNO >= N)
             return;  // (a part past the bottom or right edge of a partial tile)
     } else if (p.dp == 0u) {
-        tile_split_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, S, p.group_m, tmi, tni, ks);
+        tile_split_coords(bid, nblocks, tiles_m, tiles_n, S, p.group_m, tmi, tni, ks);
         stile = tmi * tiles_n + tni;
-    } else if (blockIdx.x < p.dp) {
-        tile_coords(blockIdx.x, p.dp, tiles_m, tiles_n, p.group_m, tmi, tni);
+    } else if (bid < p.dp) {
+        tile_coords(bid, p.dp, tiles_m, tiles_n, p.group_m, tmi, tni);
         S = 1u;
         stile = 0u;
     } else {
         const uint32_t R = tiles_m * tiles_n - p.dp;  // tiles split, S workgroups each
-        const uint32_t idx = xcd_remap(blockIdx.x - p.dp, gridDim.x - p.dp);
+        const uint32_t idx = xcd_remap(bid - p.dp, nblocks - p.dp);
         ks = idx / R;
         stile = idx - ks * R;
         group_walk(p.dp + stile, tiles_m, tiles_n, p.group_m, tmi, tni);
@@ -823,6 +829,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
             }
         }
     }
+}
+
+template <int E, int O, int BM, int BN, int RB, int NH, int WM = 2, int WN = 2, int BL = B_KCONTIG,
+          int EPI = EPI_STORE, int AL = A_KCONTIG, class P = TileArgs>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_nt(P p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[nt_lds_bytes<BM, BN, RB, NH>()];
+    gemm_nt_body<E, O, BM, BN, RB, NH, WM, WN, BL, EPI, AL, P>(p, blockIdx.x, gridDim.x, lds);
 }
 
 }  // namespace tg

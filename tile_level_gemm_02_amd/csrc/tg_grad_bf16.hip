@@ -12,6 +12,13 @@ tg_status xgrad_bf16(const TileArgs& t, void* ws, int64_t ws_bytes, void* stream
     return xgrad_typed<E_BF16>(t, ws, ws_bytes, stream);
 }
 
+tg_status group_bf16(const TileArgs* t, int n, int w_dtype, void* ws, int64_t ws_bytes, void* stream, bool* taken)
+{
+    return group_typed<E_BF16>(t, n, w_dtype, ws, ws_bytes, stream, taken);
+}
+
+int64_t group_ws_bytes_bf16(const TileArgs* t, int n) { return group_ws_bytes<E_BF16>(t, n); }
+
 tg_status glu_dgu_bf16(const TileArgs& t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream)
 {
     return glu_dgu_typed<E_BF16>(t, e, ws, ws_bytes, stream);

@@ -19,6 +19,10 @@ int64_t wgrad_ws_bytes_f16(int64_t N, int64_t K, int64_t M);
 int64_t wgrad_ws_bytes_bf16(int64_t N, int64_t K, int64_t M);
 tg_status xgrad_f16(Prod t, void* ws, int64_t ws_bytes, void* stream);
 tg_status xgrad_bf16(Prod t, void* ws, int64_t ws_bytes, void* stream);
+tg_status group_f16(const TileArgs* t, int n, int w_dtype, void* ws, int64_t ws_bytes, void* stream, bool* taken);
+tg_status group_bf16(const TileArgs* t, int n, int w_dtype, void* ws, int64_t ws_bytes, void* stream, bool* taken);
+int64_t group_ws_bytes_f16(const TileArgs* t, int n);
+int64_t group_ws_bytes_bf16(const TileArgs* t, int n);
 tg_status glu_dgu_f16(Prod t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream);
 tg_status glu_dgu_bf16(Prod t, const EpiArgs& e, void* ws, int64_t ws_bytes, void* stream);
 tg_status dz_f16(const DzArgs& p, void* ws, int64_t ws_bytes, void* stream);
@@ -47,11 +51,38 @@ static int64_t glu_ws(int in, int64_t M, int64_t F, int64_t D)
     }
 }
 
+// Workspace of a backward pass's products, t[0] being dX's and t[1 .. n-1]
+// weight gradients: the most of the grouped launch and of each product by
+// itself (a call that leaves an output out runs them one by one).
+static int64_t products_ws(int in, const TileArgs* t, int n)
+{
+    int64_t most = in == TG_IN_F16 ? group_ws_bytes_f16(t, n) : group_ws_bytes_bf16(t, n);
+    for (int i = 0; i < n; ++i)
+        most = larger(most, i == 0 ? ex_workspace_bytes(in, t[i].M, t[i].N, t[i].K, TG_ROW_MAJOR)
+                                   : wgrad_ws(in, t[i].M, t[i].N, t[i].K));
+    return most;
+}
+
+// A product of the workspace queries: rows as wide as its matrices
+static TileArgs sizes(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb)
+{
+    TileArgs t{};
+    t.M = M;
+    t.N = N;
+    t.K = K;
+    t.lda = lda;
+    t.ldb = ldb;
+    return t;
+}
+
 static int64_t linear_bwd_ws(int in, int64_t M, int64_t N, int64_t K)
 {
     if (M < 0 || N < 0 || K < 0 || (in != TG_IN_F16 && in != TG_IN_BF16))
         return -1;
-    return larger(larger(ex_workspace_bytes(in, M, K, N, TG_ROW_MAJOR), wgrad_ws(in, N, K, M)), dz_ws_bytes(M, N));
+    if (!dims_fit(M, N, K))
+        return 0;
+    const TileArgs t[] = {sizes(M, K, N, N, K), sizes(N, K, M, N, K)};
+    return larger(products_ws(in, t, 2), dz_ws_bytes(M, N));
 }
 
 static int64_t glu_bwd_ws(int in, int64_t M, int64_t F, int64_t D)
@@ -60,29 +91,38 @@ static int64_t glu_bwd_ws(int in, int64_t M, int64_t F, int64_t D)
         return -1;
     if (!dims_fit(M, F, D) || !dims_fit(2 * F, 0, 0))
         return 0;
-    return larger(larger(ex_workspace_bytes(in, M, F, D, TG_ROW_MAJOR), ex_workspace_bytes(in, M, D, 2 * F, TG_ROW_MAJOR)),
-                  larger(wgrad_ws(in, 2 * F, D, M), wgrad_ws(in, D, F, M)));
+    const TileArgs t[] = {sizes(M, D, 2 * F, 2 * F, D), sizes(2 * F, D, M, 2 * F, D), sizes(D, F, M, D, F)};
+    return larger(products_ws(in, t, 3), ex_workspace_bytes(in, M, F, D, TG_ROW_MAJOR));
 }
 
-// C (M x N) = A . B with B row-major
-static tg_status product_row(int in, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
-                             int64_t ldb, void* C, int64_t ldc, void* ws, int64_t ws_bytes, void* stream)
+// The products of a backward pass: t[0] is dX's (A . B with B row-major),
+// t[1 .. n-1] are weight gradients (A^T . B, A stored K x M and B K x N); an
+// output that was left out has C null.  All in one launch where that is
+// taken, else one by one.
+static tg_status products(int in, const TileArgs* t, int n, int w_dtype, void* ws, int64_t ws_bytes, void* stream)
 {
-    TileArgs t{};
-    set_product(t, M, N, K, A, lda, B, ldb, C, ldc, 1.0f);
-    return in == TG_IN_F16 ? xgrad_f16(t, ws, ws_bytes, stream) : xgrad_bf16(t, ws, ws_bytes, stream);
-}
-
-// C (M x N) = A^T . B with A stored K x M and B stored K x N
-static tg_status product_tn(int in, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
-                            int64_t ldb, void* C, int64_t ldc, int c_dtype, void* ws, int64_t ws_bytes, void* stream)
-{
-    if (M == 0 || N == 0)
-        return TG_OK;
-    TileArgs t{};
-    set_product(t, M, N, K, A, lda, B, ldb, C, ldc, 1.0f);
-    return in == TG_IN_F16 ? wgrad_f16(t, c_dtype, ws, ws_bytes, stream)
-                           : wgrad_bf16(t, c_dtype, ws, ws_bytes, stream);
+    bool all = true, taken = false;
+    for (int i = 0; i < n; ++i)
+        all = all && t[i].C != nullptr;
+    if (all) {
+        const tg_status st = in == TG_IN_F16 ? group_f16(t, n, w_dtype, ws, ws_bytes, stream, &taken)
+                                             : group_bf16(t, n, w_dtype, ws, ws_bytes, stream, &taken);
+        if (taken || st != TG_OK)
+            return st;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (t[i].C == nullptr || t[i].M == 0 || t[i].N == 0)
+            continue;
+        tg_status st;
+        if (i == 0)
+            st = in == TG_IN_F16 ? xgrad_f16(t[i], ws, ws_bytes, stream) : xgrad_bf16(t[i], ws, ws_bytes, stream);
+        else
+            st = in == TG_IN_F16 ? wgrad_f16(t[i], w_dtype, ws, ws_bytes, stream)
+                                 : wgrad_bf16(t[i], w_dtype, ws, ws_bytes, stream);
+        if (st != TG_OK)
+            return st;
+    }
+    return TG_OK;
 }
 
 // first failing status of a list
@@ -215,14 +255,10 @@ extern "C" tg_status tg_linear_backward(tg_input in_arg, int64_t M, int64_t N, i
     }
     const void* d = act == TG_ACT_NONE ? dY : dZ;
     const int64_t ldd = act == TG_ACT_NONE ? lddy : lddz;
-    if (dX != nullptr && M > 0 && K > 0) {
-        bad = product_row(in, M, K, N, d, ldd, W, ldw, dX, lddx, workspace, workspace_bytes, stream);
-        if (bad != TG_OK)
-            return bad;
-    }
-    if (dW != nullptr)
-        return product_tn(in, N, K, M, d, ldd, x, ldx, dW, lddw, dw_dtype, workspace, workspace_bytes, stream);
-    return TG_OK;
+    TileArgs t[2] = {};
+    set_product(t[0], M, K, N, d, ldd, W, ldw, dX, lddx, 1.0f);
+    set_product(t[1], N, K, M, d, ldd, x, ldx, dW, lddw, 1.0f);
+    return products(in, t, 2, dw_dtype, workspace, workspace_bytes, stream);
 }
 
 extern "C" tg_status tg_glu(tg_input in_arg, int64_t M, int64_t F, int64_t D, const void* x, int64_t ldx,
@@ -308,18 +344,9 @@ extern "C" tg_status tg_glu_backward(tg_input in_arg, int64_t M, int64_t F, int6
         if (bad != TG_OK)
             return bad;
     }
-    if (dX != nullptr && M > 0 && D > 0) {
-        bad = product_row(in, M, D, 2 * F, dgate_up, lddgu, W, ldw, dX, lddx, workspace, workspace_bytes, stream);
-        if (bad != TG_OK)
-            return bad;
-    }
-    if (dW != nullptr) {
-        bad = product_tn(in, 2 * F, D, M, dgate_up, lddgu, x, ldx, dW, lddw, dw_dtype, workspace, workspace_bytes,
-                         stream);
-        if (bad != TG_OK)
-            return bad;
-    }
-    if (dWd != nullptr)
-        return product_tn(in, D, F, M, dY, lddy, H, ldh, dWd, lddwd, dw_dtype, workspace, workspace_bytes, stream);
-    return TG_OK;
+    TileArgs t[3] = {};
+    set_product(t[0], M, D, 2 * F, dgate_up, lddgu, W, ldw, dX, lddx, 1.0f);
+    set_product(t[1], 2 * F, D, M, dgate_up, lddgu, x, ldx, dW, lddw, 1.0f);
+    set_product(t[2], D, F, M, dY, lddy, H, ldh, dWd, lddwd, 1.0f);
+    return products(in, t, 3, dw_dtype, workspace, workspace_bytes, stream);
 }
