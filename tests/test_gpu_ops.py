@@ -95,8 +95,8 @@ def linear_case(tg, M, N, K, dt, od, name, bias, res, keep, ws, seed=1):
 
 # matrix-vector sized calls: one and two slices of rows, K tails, narrow N (K split over workgroups), odd N
 @pytest.mark.parametrize("M,N,K", [(1, 129, 64), (1, 256, 8192), (7, 77, 200), (8, 512, 4096), (9, 40, 72), (16, 300, 1000),
-                                   (17, 65, 136), (32, 512, 4104)])
-@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32")])
+                                   (17, 65, 136), (32, 512, 4104), (3, 8201, 136), (13, 8190, 72)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32"), ("fp8", "bf16"), ("fp8", "f32")])
 def test_linear_few_rows(tg, ws, M, N, K, dt, od):
     for w in (ws, None):
         linear_case(tg, M, N, K, dt, od, "silu", True, True, True, w)
@@ -230,11 +230,11 @@ def glu_case(tg, M, F, D, dt, od, name, keep, ws, seed=1):
 
 @pytest.mark.parametrize("M,F,D", [(1, 40, 64), (1, 128, 8192), (8, 333, 520), (9, 40, 72), (16, 512, 4104), (17, 65, 136),
                                    (32, 256, 4096)])
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
-def test_glu_few_rows(tg, ws, M, F, D, dt):
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f16"), ("fp8", "bf16")])
+def test_glu_few_rows(tg, ws, M, F, D, dt, od):
     for w in (ws, None):
-        glu_case(tg, M, F, D, dt, dt, "silu", True, w)
-        glu_case(tg, M, F, D, dt, dt, "gelu", False, w)
+        glu_case(tg, M, F, D, dt, od, "silu", True, w)
+        glu_case(tg, M, F, D, dt, od, "gelu", False, w)
 
 
 @pytest.mark.parametrize("name", ACTS)

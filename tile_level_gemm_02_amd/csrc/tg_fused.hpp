@@ -111,6 +111,13 @@ tg_status launch_fused(P& a, void* ws, int64_t ws_bytes, hipStream_t s)
     return launched();
 }
 
+// skinny_split, by the bytes of K that a workgroup streams
+template <int E>
+inline int fused_split(int64_t blocks, int64_t K)
+{
+    return skinny_split(blocks, K * ElemInfo<E>::bytes / 2, false);
+}
+
 template <int E, int O, int AI, int SPLIT, int CG, int EPI>
 void launch_skinny_epi(const FusedSkinnyArgs& sa, int64_t blocks, int split, hipStream_t s)
 {
@@ -119,12 +126,40 @@ void launch_skinny_epi(const FusedSkinnyArgs& sa, int64_t blocks, int split, hip
                        dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * G::WAVES), 0, s, sa);
 }
 
+// Rows up to which a call takes the skinny kernel.  fp8's second slice of 16
+// rows runs slower there than the tile kernel with K split (32 rows,
+// N = 8192, K = 4096: 14.8 us against 12.1; one slice, N = K = 8192: 13.5
+// against 20.5).
+template <int E>
+constexpr int64_t kFusedSkinnyRows = E == E_FP8 ? 16 : kSkSliceMaxMSplit;
+
+// 16-column groups per workgroup: two with several slices of rows, and for
+// 9 to 16 rows where that leaves a workgroup for every compute unit, since
+// each workgroup copies its rows of x over all of K (bf16 N = K = 8192: 16
+// rows 26.9 -> 25.8 us, but 1 row 24.3 -> 24.9).
+inline int fused_cg(int64_t M, int64_t N) { return M > 16 || (M > 8 && N > 32 * 255) ? 2 : 1; }
+
+inline int64_t fused_skinny_blocks(int64_t M, int64_t N)
+{
+    const int64_t cols = 16 * fused_cg(M, N);
+    const int64_t nblk = (N + cols - 1) / cols, slices = (M + 15) / 16;
+    return slices == 1 ? nblk : (nblk + 7) / 8 * 8 * slices;
+}
+
+inline int64_t fused_skinny_ws_bytes(int64_t M, int64_t N, int64_t blocks, int split)
+{
+    const int64_t groups = fused_cg(M, N);
+    if (split <= 1 || blocks * groups * 16 > kSplitMaxCounters)  // (kCounterStride words each)
+        return 0;
+    return kSplitCounterBytes + blocks * groups * split * 1024;
+}
+
 template <int E, int O, int SPLIT>
 void launch_skinny_fused(const FusedSkinnyArgs& sa, int64_t blocks, int split, hipStream_t s)
 {
     if (sa.M <= 8)
         launch_skinny_epi<E, O, 1, SPLIT, 1, EPI_LINEAR>(sa, blocks, split, s);
-    else if (skinny_cg(sa.M) == 1)
+    else if (fused_cg(sa.M, sa.N) == 1)
         launch_skinny_epi<E, O, 2, SPLIT, 1, EPI_LINEAR>(sa, blocks, split, s);
     else
         launch_skinny_epi<E, O, 2, SPLIT, 2, EPI_LINEAR>(sa, blocks, split, s);
@@ -140,39 +175,50 @@ void launch_skinny_glu(const FusedSkinnyArgs& sa, int64_t blocks, int split, hip
 }
 
 // ------------------------------------------------------------------ linear
+template <int E>
+int64_t linear_ws_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || !dims_fit(M, N, K))
+        return 0;
+    if (M <= kFusedSkinnyRows<E>) {
+        const int64_t blocks = fused_skinny_blocks(M, N);
+        return fused_skinny_ws_bytes(M, N, blocks, fused_split<E>(blocks, K));
+    }
+    return K % (16 / ElemInfo<E>::bytes) == 0 ? plan_nt<E, B_KCONTIG>(M, N, K, true).ws_bytes : 0;
+}
+
 template <int E, int O>
 tg_status linear_out(FusedArgs& a, void* ws, int64_t ws_bytes, hipStream_t s)
 {
-    if constexpr (E != E_FP8) {
-        if (a.M <= kSkSliceMaxMSplit && a.K > 0 &&
-            skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, skinny_cg(a.M))) {
-            FusedSkinnyArgs sa{};
-            sa.M = a.M;
-            sa.N = a.N;
-            sa.K = a.K;
-            sa.A = a.A;
-            sa.lda = a.lda;
-            sa.B = a.B;
-            sa.ldb = a.ldb;
-            sa.C = a.C;
-            sa.ldc = a.ldc;
-            sa.e = a.e;
-            const int64_t blocks = skinny_blocks(a.M, a.N);
-            if (blocks > 0x7FFFFFFF)
-                return TG_ERR_NOT_SUPPORTED;
-            int split = skinny_split(blocks, a.K, false);
-            const int64_t need = split > 1 ? skinny_ws_bytes(a.M, blocks, split) : 0;
-            if (ws == nullptr || need == 0 || need > ws_bytes)
-                split = 1;
-            if (split > 1) {
-                sa.counters = (uint32_t*)ws;
-                sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
-                launch_skinny_fused<E, O, 2>(sa, blocks, split, s);
-            } else {
-                launch_skinny_fused<E, O, 0>(sa, blocks, 1, s);
-            }
-            return launched();
+    if (a.M <= kFusedSkinnyRows<E> && a.K > 0 &&
+        skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, fused_cg(a.M, a.N))) {
+        FusedSkinnyArgs sa{};
+        sa.M = a.M;
+        sa.N = a.N;
+        sa.K = a.K;
+        sa.A = a.A;
+        sa.lda = a.lda;
+        sa.B = a.B;
+        sa.ldb = a.ldb;
+        sa.C = a.C;
+        sa.ldc = a.ldc;
+        sa.e = a.e;
+        sa.alpha = a.alpha;
+        const int64_t blocks = fused_skinny_blocks(a.M, a.N);
+        if (blocks > 0x7FFFFFFF)
+            return TG_ERR_NOT_SUPPORTED;
+        int split = fused_split<E>(blocks, a.K);
+        const int64_t need = fused_skinny_ws_bytes(a.M, a.N, blocks, split);
+        if (ws == nullptr || need == 0 || need > ws_bytes)
+            split = 1;
+        if (split > 1) {
+            sa.counters = (uint32_t*)ws;
+            sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+            launch_skinny_fused<E, O, 2>(sa, blocks, split, s);
+        } else {
+            launch_skinny_fused<E, O, 0>(sa, blocks, 1, s);
         }
+        return launched();
     }
     return launch_fused<E, O, B_KCONTIG, EPI_LINEAR, A_KCONTIG>(a, ws, ws_bytes, s);
 }
@@ -205,7 +251,7 @@ inline int64_t glu_skinny_blocks(int64_t M, int64_t F)
 
 inline int64_t glu_skinny_ws_bytes(int64_t blocks, int split)
 {
-    return split <= 1 || blocks > kSplitMaxCounters ? 0 : kSplitCounterBytes + blocks * split * 2048;
+    return split <= 1 || blocks * 16 > kSplitMaxCounters ? 0 : kSplitCounterBytes + blocks * split * 2048;
 }
 
 template <int E>
@@ -213,9 +259,9 @@ int64_t glu_ws_bytes(int64_t M, int64_t F, int64_t D)
 {
     if (M <= 0 || F <= 0 || D <= 0 || !dims_fit(M, 2 * F, D))
         return 0;
-    if (E != E_FP8 && M <= kSkSliceMaxMSplit) {
+    if (M <= kFusedSkinnyRows<E>) {
         const int64_t blocks = glu_skinny_blocks(M, F);
-        return glu_skinny_ws_bytes(blocks, skinny_split(blocks, D, false));
+        return glu_skinny_ws_bytes(blocks, fused_split<E>(blocks, D));
     }
     return D % (16 / ElemInfo<E>::bytes) == 0 ? plan_nt<E, B_KCONTIG>(M, 2 * F, D, true).ws_bytes : 0;
 }
@@ -223,35 +269,34 @@ int64_t glu_ws_bytes(int64_t M, int64_t F, int64_t D)
 template <int E, int O>
 tg_status glu_out(FusedArgs& a, void* ws, int64_t ws_bytes, hipStream_t s)
 {
-    if constexpr (E != E_FP8) {
-        if (a.M <= kSkSliceMaxMSplit && a.K > 0 && skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, 1)) {
-            FusedSkinnyArgs sa{};
-            sa.M = a.M;
-            sa.N = a.N;
-            sa.K = a.K;
-            sa.A = a.A;
-            sa.lda = a.lda;
-            sa.B = a.B;
-            sa.ldb = a.ldb;
-            sa.C = a.C;
-            sa.ldc = a.ldc;
-            sa.e = a.e;
-            const int64_t blocks = glu_skinny_blocks(a.M, a.N);
-            if (blocks > 0x7FFFFFFF)
-                return TG_ERR_NOT_SUPPORTED;
-            int split = skinny_split(blocks, a.K, false);
-            const int64_t need = glu_skinny_ws_bytes(blocks, split);
-            if (ws == nullptr || need == 0 || need > ws_bytes)
-                split = 1;
-            if (split > 1) {
-                sa.counters = (uint32_t*)ws;
-                sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
-                launch_skinny_glu<E, O, 2>(sa, blocks, split, s);
-            } else {
-                launch_skinny_glu<E, O, 0>(sa, blocks, 1, s);
-            }
-            return launched();
+    if (a.M <= kFusedSkinnyRows<E> && a.K > 0 && skinny_offsets_fit(a.K, a.lda, a.ldb, SkinnyCfg::RING, 1)) {
+        FusedSkinnyArgs sa{};
+        sa.M = a.M;
+        sa.N = a.N;
+        sa.K = a.K;
+        sa.A = a.A;
+        sa.lda = a.lda;
+        sa.B = a.B;
+        sa.ldb = a.ldb;
+        sa.C = a.C;
+        sa.ldc = a.ldc;
+        sa.e = a.e;
+        sa.alpha = a.alpha;
+        const int64_t blocks = glu_skinny_blocks(a.M, a.N);
+        if (blocks > 0x7FFFFFFF)
+            return TG_ERR_NOT_SUPPORTED;
+        int split = fused_split<E>(blocks, a.K);
+        const int64_t need = glu_skinny_ws_bytes(blocks, split);
+        if (ws == nullptr || need == 0 || need > ws_bytes)
+            split = 1;
+        if (split > 1) {
+            sa.counters = (uint32_t*)ws;
+            sa.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+            launch_skinny_glu<E, O, 2>(sa, blocks, split, s);
+        } else {
+            launch_skinny_glu<E, O, 0>(sa, blocks, 1, s);
         }
+        return launched();
     }
     return launch_fused<E, O, B_KCONTIG, EPI_GLU, A_KCONTIG>(a, ws, ws_bytes, s);
 }

@@ -22,6 +22,8 @@
 // as zeros), lane quarter h = l/16 takes k = 8h .. 8h+7 of each 32.  The
 // result lane l, value v is row l%16, column 4*(l/16) + v.
 //
+// fp8 inputs (with a fused epilogue): the same rows of 128 bytes hold 128 k.
+//
 // A K tail (K % 64) is multiplied after the ring by one wave, from global
 // memory with element masks.
 #pragma once
@@ -70,7 +72,9 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
     static_assert(!GLU || CG == 2, "a gate group and an up group");
     static_assert(EPI == EPI_STORE || SPLIT != 1, "an epilogue needs the whole sum");
     typedef typename OutInfo<O>::T OutT;
-    static_assert(E == E_F16 || E == E_BF16, "16-bit inputs");
+    static_assert(E == E_F16 || E == E_BF16 || EPI != EPI_STORE, "fp8 takes a fused epilogue's scale");
+    constexpr int EB = ElemInfo<E>::bytes, CE = 16 / EB;
+    constexpr int KES = kSkRow / EB, KEB = KES / 2;  // elements per stage, and per row of one matrix step
     static_assert(SPLIT != 1 || O == O_F32, "partial tiles are added in fp32");
     constexpr int SLOT = SkinnySlot<AI, CG>::BYTES;
     constexpr int COLS = 16 * CG;          // columns (B rows) per workgroup
@@ -96,8 +100,8 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
     if (n0 >= N)
         return;  // padding of the last group of eight column blocks (whole workgroup)
     const int64_t M = p.M - 16 * slice < 16 ? p.M - 16 * slice : 16;  // rows of this slice
-    const uint8_t* const Ab = p.A + 16 * slice * p.lda * 2;
-    const int64_t KS = K / kSkKE;  // whole stages
+    const uint8_t* const Ab = p.A + 16 * slice * p.lda * EB;
+    const int64_t KS = K / KES;  // whole stages
     // this workgroup's stages [z0, z1), split over its waves in contiguous ranges
     const int64_t z0 = SPLIT != 0 ? KS * blockIdx.y / gridDim.y : 0;
     const int64_t z1 = SPLIT != 0 ? KS * (blockIdx.y + 1) / gridDim.y : KS;
@@ -112,18 +116,18 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
     // out-of-range offset (zeros).  The host guarantees every valid offset,
     // plus the stage offsets the ring forms, stays below 2^31.
     const i32x4_t ra = make_rsrc(Ab);
-    const i32x4_t rb = make_rsrc(p.B + n0 * p.ldb * 2);
-    const i32x4_t rup = make_rsrc(GLU ? p.B + (N + n0) * p.ldb * 2 : p.B);
+    const i32x4_t rb = make_rsrc(p.B + n0 * p.ldb * EB);
+    const i32x4_t rup = make_rsrc(GLU ? p.B + (N + n0) * p.ldb * EB : p.B);
     uint32_t vb[BI], va[AI];
 #pragma unroll
     for (int i = 0; i < BI; ++i) {
         const uint32_t r = 8u * i + lane / 8u, rr = GLU ? r % 16u : r;
-        vb[i] = n0 + rr < N ? rr * (uint32_t)p.ldb * 2u + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
+        vb[i] = n0 + rr < N ? rr * (uint32_t)p.ldb * (uint32_t)EB + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
     }
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
         const uint32_t r = 8u * i + lane / 8u;
-        va[i] = (int64_t)r < M ? r * (uint32_t)p.lda * 2u + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
+        va[i] = (int64_t)r < M ? r * (uint32_t)p.lda * (uint32_t)EB + sk_swz(r, lane % 8u) * 16u : kOutOfRange;
     }
     const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + wave * (RING * SLOT);
     // B rows read by this workgroup alone (one slice) stream with the
@@ -191,21 +195,21 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
 
     // the K tail (K % 64: at most two 32-wide blocks, the last one partial),
     // taken by one wave of the workgroup that holds the end of K
-    if (K % kSkKE != 0 && wave == WAVES - 1 && (SPLIT == 0 || blockIdx.y == gridDim.y - 1)) {
-        for (int64_t kb = KS * 2; kb * 32 < K; ++kb) {
-            const int64_t k = kb * 32 + h * 8;
+    if (K % KES != 0 && wave == WAVES - 1 && (SPLIT == 0 || blockIdx.y == gridDim.y - 1)) {
+        for (int64_t kb = KS * 2; kb * KEB < K; ++kb) {
+            const int64_t k = kb * KEB + h * CE;
             u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
             if ((int64_t)c16 < M && k < K) {
-                const uint8_t* src = Ab + ((int64_t)c16 * p.lda + k) * 2;
-                a = (k + 8 <= K) ? ldg128(src) : load_chunk_partial<2>(src, K - k);
+                const uint8_t* src = Ab + ((int64_t)c16 * p.lda + k) * EB;
+                a = (k + CE <= K) ? ldg128(src) : load_chunk_partial<EB>(src, K - k);
             }
 #pragma unroll
             for (int g = 0; g < CG; ++g) {
                 const int64_t n = n0 + (GLU ? 0 : 16 * g) + c16;
                 b = u32x4{0u, 0u, 0u, 0u};
                 if (n < N && k < K) {
-                    const uint8_t* src = p.B + ((GLU && g == 1 ? N + n : n) * p.ldb + k) * 2;
-                    b = (k + 8 <= K) ? ldg128(src) : load_chunk_partial<2>(src, K - k);
+                    const uint8_t* src = p.B + ((GLU && g == 1 ? N + n : n) * p.ldb + k) * EB;
+                    b = (k + CE <= K) ? ldg128(src) : load_chunk_partial<EB>(src, K - k);
                 }
                 acc[g][0] = Mfma16<E>::run(b, a, acc[g][0]);
             }
@@ -269,6 +273,10 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
                             }
                 }
             }
+            if constexpr (E == E_FP8)
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+                    sum[q] *= p.alpha;
             const int64_t row = 16 * slice + c16, col0 = n0 + (GLU ? 0 : 16 * wave) + 4 * h;
             if ((int64_t)c16 < M)
                 for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {

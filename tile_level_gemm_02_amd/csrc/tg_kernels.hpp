@@ -412,6 +412,7 @@ struct SkinnyArgs {
 // with a fused epilogue (EPI_LINEAR, EPI_GLU)
 struct FusedSkinnyArgs : SkinnyArgs {
     EpiArgs e;
+    float alpha;  // fp8 only
 };
 
 template <int E> struct Mfma16;
@@ -425,6 +426,18 @@ template <> struct Mfma16<E_BF16> {
     __device__ __forceinline__ static f32x4 run(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(bit_cast<bf16x8>(a), bit_cast<bf16x8>(b), c, 0, 0, 0);
+    }
+};
+
+// 16 fp8 values per lane: two 16x16x32 products (the k order does not matter,
+// both operands carrying the same k in the same place)
+template <> struct Mfma16<E_FP8> {
+    __device__ __forceinline__ static f32x4 run(u32x4 a, u32x4 b, f32x4 c)
+    {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(bit_cast<long>(u32x2{a[0], a[1]}), bit_cast<long>(u32x2{b[0], b[1]}), c,
+                                                       0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(bit_cast<long>(u32x2{a[2], a[3]}), bit_cast<long>(u32x2{b[2], b[3]}),
+                                                          c, 0, 0, 0);
     }
 };
 

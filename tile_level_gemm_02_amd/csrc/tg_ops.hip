@@ -7,6 +7,9 @@ typedef const TileArgs& Prod;
 tg_status linear_f16(Prod t, const EpiArgs& e, int y_dtype, void* ws, int64_t ws_bytes, void* stream);
 tg_status linear_bf16(Prod t, const EpiArgs& e, int y_dtype, void* ws, int64_t ws_bytes, void* stream);
 tg_status linear_fp8(Prod t, const EpiArgs& e, int y_dtype, void* ws, int64_t ws_bytes, void* stream);
+int64_t linear_ws_bytes_f16(int64_t M, int64_t N, int64_t K);
+int64_t linear_ws_bytes_bf16(int64_t M, int64_t N, int64_t K);
+int64_t linear_ws_bytes_fp8(int64_t M, int64_t N, int64_t K);
 tg_status glu_f16(Prod t, const EpiArgs& e, int h_dtype, void* ws, int64_t ws_bytes, void* stream);
 tg_status glu_bf16(Prod t, const EpiArgs& e, int h_dtype, void* ws, int64_t ws_bytes, void* stream);
 tg_status glu_fp8(Prod t, const EpiArgs& e, int h_dtype, void* ws, int64_t ws_bytes, void* stream);
@@ -37,6 +40,18 @@ static int elem_bytes(int in) { return in == TG_IN_FP8 ? 1 : 2; }
 static int64_t wgrad_ws(int in, int64_t N, int64_t K, int64_t M)
 {
     return in == TG_IN_F16 ? wgrad_ws_bytes_f16(N, K, M) : wgrad_ws_bytes_bf16(N, K, M);
+}
+
+static int64_t linear_ws(int in, int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return -1;
+    switch (in) {
+    case TG_IN_F16: return linear_ws_bytes_f16(M, N, K);
+    case TG_IN_BF16: return linear_ws_bytes_bf16(M, N, K);
+    case TG_IN_FP8: return linear_ws_bytes_fp8(M, N, K);
+    default: return -1;
+    }
 }
 
 static int64_t glu_ws(int in, int64_t M, int64_t F, int64_t D)
@@ -141,7 +156,7 @@ using namespace tg;
 
 extern "C" int64_t tg_linear_workspace_bytes(tg_input in, int64_t M, int64_t N, int64_t K)
 {
-    return ex_workspace_bytes(abi_int(in), M, N, K, TG_COL_MAJOR);
+    return linear_ws(abi_int(in), M, N, K);
 }
 
 extern "C" int64_t tg_linear_backward_workspace_bytes(tg_input in, int64_t M, int64_t N, int64_t K)
@@ -182,7 +197,7 @@ extern "C" tg_status tg_linear(tg_input in_arg, int64_t M, int64_t N, int64_t K,
         residual == nullptr ? TG_OK : check_mat(residual, M, N, ldr, ob),
         preact == nullptr ? TG_OK : check_mat(preact, M, N, ldz, ob),
         ((uintptr_t)bias & 3u) ? TG_ERR_MISALIGNED : TG_OK,
-        check_ws(workspace, workspace_bytes, workspace == nullptr ? 0 : ex_workspace_bytes(in, M, N, K, TG_COL_MAJOR)),
+        check_ws(workspace, workspace_bytes, workspace == nullptr ? 0 : linear_ws(in, M, N, K)),
     };
     const tg_status bad = first_error(st, sizeof st / sizeof st[0]);
     if (bad != TG_OK || M == 0 || N == 0)
