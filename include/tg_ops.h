@@ -13,9 +13,9 @@
  * nn.Linear layout, as TG_COL_MAJOR in tg.h).  All sums, activations and
  * their derivatives are fp32 on the unrounded accumulator; every stored value
  * is rounded once, to nearest even.  fp8 inputs (OCP e4m3) carry per-tensor
- * scales; their matrix instruction sums each group of 8 products to about 13
- * bits below the largest (see tg_gemm_fp8's use in tg.h), so fp32 outputs of
- * fp8 inputs hold about four digits.
+ * scales; their matrix instructions sum each group of 8 products to about 13
+ * bits below the largest, so fp32 outputs of fp8 inputs hold about four
+ * digits.
  *
  * workspace: as for tg_gemm_ex (256-byte aligned device memory, first 64 KiB
  * zero before first use and left zero, one per concurrently running call, or

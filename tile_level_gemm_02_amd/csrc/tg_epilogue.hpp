@@ -25,6 +25,14 @@
 //
 // The paths (kinds) are told apart by a uniform branch outside the loops over
 // a tile's values, so that one kernel serves every activation.
+//
+// What an epilogue costs, per round of 256 x 256 tiles at K = 4096 (4096 x
+// 16384 outputs, bf16, a round of the bare product about 90 us): storing
+// through fp32 rows 6 us, with a residual or with gelu and a kept
+// pre-activation 13, the gated product 2, with both projections kept 10.  The
+// stores themselves are hidden (all tiles writing one region: 1 us less); what
+// remains is the rows' way through LDS and the operands' latency, which a
+// compute unit holding one workgroup cannot overlap with another tile.
 #pragma once
 
 #include <type_traits>

@@ -429,9 +429,12 @@ tg_status launch_nt_plan(P& a, const NtPlan& plan, void* ws, hipStream_t s)
             return launch_nt<E, O, 64, 64, BL, 8, EPI, AL>(b, 1, s, 16 * rest);
     }
     if (plan.tile == 256 && plan.tn == 128) {
+        // (plan_nt gives this tile kWideNH slots; the four-slot build is the plain GEMM's alone)
+        if constexpr (!std::is_same<P, TileArgs>::value)
+            return launch_nt<E, O, 256, 128, BL, kWideNH, EPI, AL>(a, plan.splits, s);
         if (plan.nh == 6)
-            return launch_nt<E, O, 256, 128, BL, 6, EPI, AL>(a, plan.splits, s);
-        return launch_nt<E, O, 256, 128, BL, 4, EPI, AL>(a, plan.splits, s);
+            return launch_nt<E, O, 256, 128, BL, 6>(a, plan.splits, s);
+        return launch_nt<E, O, 256, 128, BL, 4>(a, plan.splits, s);
     }
     if (plan.tile == 256) {
         if (plan.nh == 5)
