@@ -384,6 +384,47 @@ def test_infinities_and_nan(tg, ws):
                 assert bool(torch.isnan(y[3]).all()) and bool(torch.isnan(h[3]).all())
 
 
+def test_offsets_past_32_bits(tg, ws):
+    """Outputs of more than 2^31 elements, reductions over more than 2^31 bytes
+    of rows, and gradients of more than 2^31 elements."""
+    t = torch.bfloat16
+    M, N, K = 530_000, 4104, 64
+    x, w, r = rand(M, K, t, 1), rand(N, K, t, 2, K ** -0.5), rand(300, N, t, 3)
+    y = torch.full((M + 2, N), MARK, device="cuda", dtype=t)
+    res = y[:M]
+    res[-300:] = r  # the residual in place: the last rows lie past 2^31 elements
+    tg.tg_linear(x, w, res, act="silu", residual=res, workspace=ws)
+    for rows, add in ((slice(0, 300), MARK), (slice(M - 300, M), r.double())):
+        z, tol = product(x[rows], w)
+        v = act("silu", z)[0]
+        tol, v = act_bound("silu", z, v, tol), v + add
+        within(res[rows], v, (tol + 2 * U * v.abs()) * (1 + 2.0 ** -7) + rounding(v, t), "y")
+    assert bool((y[M:] == MARK).all())
+    del y, res
+    M, N, K = 200_000, 8200, 72
+    dy, x, w = rand(M, N, t, 1), rand(M, K, t, 2), rand(N, K, t, 3)  # dy: 3.3 GB
+    dw, db = torch.empty(N, K, device="cuda"), torch.empty(N, device="cuda")
+    tg.tg_linear_backward(dy, x, w, dw=dw, dbias=db, workspace=ws)
+    want, size, total, amount = 0.0, 0.0, 0.0, 0.0
+    for i in range(0, M, 20_000):
+        a, b = dy[i:i + 20_000].double().t().contiguous(), x[i:i + 20_000].double()
+        want, size, total, amount = want + a @ b, size + a.abs() @ b.abs(), total + a.sum(1), amount + a.abs().sum(1)
+    # fp32 sums of M values: M u S bounds any order, the sums are of M / 64 or fewer in a row
+    within(dw, want, 2 * M * U * size, "dw")
+    within(db, total, M * U * amount, "dbias")
+    del dy, want, size
+    n = (1 << 31) + 77
+    g, norm = torch.full((n,), 0.5, device="cuda", dtype=t), torch.empty(1, device="cuda")
+    g[-1] = -0.25
+    tg.tg_clip_grads([g], 1e9, norm=norm, workspace=ws)
+    want = ((n - 1) * 0.25 + 0.0625) ** 0.5
+    assert abs(float(norm) - want) <= 2 * U * want and float(g[-1]) == -0.25
+    tg.tg_clip_grads([g], 0.5 * want, norm=norm, workspace=ws)
+    for i in (0, (1 << 31) - 1, 1 << 31, n - 2):
+        assert float(g[i]) == 0.25
+    assert float(g[-1]) == -0.125
+
+
 # ------------------------------------------------------------------- clipping
 
 

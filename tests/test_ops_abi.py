@@ -169,6 +169,7 @@ def test_binding_refuses_wrong_tensors(tg):
     no(tg.tg_linear, x, w, y, residual=t(4, 8))
     no(tg.tg_linear, x, w, y, preact=t(4, 7, dtype=bf))
     no(tg.tg_linear, t(16, dtype=bf), w, y)
+    no(tg.tg_linear, x, t((), dtype=bf), y)
     no(tg.tg_linear_backward, y, x, w, preact=y, act="silu")
     no(tg.tg_linear_backward, y.to(f8), x, w)
     no(tg.tg_linear_backward, y, x, w, dw=t(8, 16, dtype=f16))

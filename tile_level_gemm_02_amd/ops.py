@@ -208,7 +208,7 @@ def tg_linear(x, W, Y, bias=None, act: str = "none", residual=None, preact=None,
     """Y = act(z) + residual, z = scale_x scale_w x . W^T + bias; z is kept in ``preact`` if given."""
     i = _input(x, "tg_linear")
     M, K = _2d(x, "x")
-    N = W.shape[0]
+    N = _2d(W, "W")[0]
     a = _act(act)
     dev = _device(x, "x")
     own = _OWN[x.dtype]
