@@ -257,7 +257,7 @@ inline int64_t glu_skinny_ws_bytes(int64_t blocks, int split)
 template <int E>
 int64_t glu_ws_bytes(int64_t M, int64_t F, int64_t D)
 {
-    if (M <= 0 || F <= 0 || D <= 0 || !dims_fit(M, 2 * F, D))
+    if (M <= 0 || F <= 0 || D <= 0 || !dims_fit(M, F, D) || !dims_fit(2 * F, 0, 0))
         return 0;
     if (M <= kFusedSkinnyRows<E>) {
         const int64_t blocks = glu_skinny_blocks(M, F);
