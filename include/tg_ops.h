@@ -17,6 +17,11 @@
  * bits below the largest, so fp32 outputs of fp8 inputs hold about four
  * digits.
  *
+ * Speed: sums that run along a matrix's rows take fast kernels where the rows
+ * fill whole 16-byte chunks (multiples of 8 elements, 16 for fp8), and so do
+ * the column counts of the gradients' products; other sizes run a tile kernel
+ * that is several times slower.
+ *
  * workspace: as for tg_gemm_ex (256-byte aligned device memory, first 64 KiB
  * zero before first use and left zero, one per concurrently running call, or
  * NULL with workspace_bytes 0: less is split then).  One workspace of the

@@ -412,20 +412,34 @@ GroupPlan plan_group(const TileArgs* t, int n, bool allow_split)
     return p;
 }
 
-// Whether a group takes these products: all on the NT kernel's grid and none
-// of a size that the 256 tile would take.
+// Whether a group takes these products: all on the NT kernel's grid, at most
+// kGroupWork tile steps together (128 for each of the 512 workgroups that run
+// at once), and none that fills half the chip with tiles of 256 over 32 steps
+// or more.  Grouped against one by one: 1024 x 6144 x 1536 (18 K steps)
+// 67 -> 64 us, 200 x 4096 x 2048 31 -> 26, gated 128 x 4096 x 2048 47 -> 41,
+// 1504 x 4000 x 1504 (45 K) 191 -> 158, 96 x 9000 x 3600 204 -> 147; what stays
+// out: 4096^3 (131 K) 260 -> 309, 7000 x 2048 x 1536 126 -> 135, for which the
+// 256 tile's fewer bytes per operation win.  (One that loses and is taken:
+// 64 x 8192 x 8192, 73 -> 85, a weight gradient of a single step.)
+constexpr int64_t kGroupWork = 65536;
+
 template <int E>
 bool group_takes(const TileArgs* t, int n)
 {
+    int64_t work = 0;
     for (int i = 0; i < n; ++i) {
         if (t[i].M <= 0 || t[i].N <= 0 || t[i].K <= 0)
             return false;
         if (!(i == 0 ? nt_eligible_nrow<E>(t[i]) : nt_eligible_tn<E>(t[i])))
             return false;
-        if (n_tiles<256, 256>(t[i].M, t[i].N) >= 128)
+        const int64_t tiles = n_tiles<kGroupTile, kGroupTile>(t[i].M, t[i].N), steps = (t[i].K + 63) / 64;
+        if (tiles > kGroupWork || steps > kGroupWork)
             return false;
+        if (steps >= 32 && n_tiles<256, 256>(t[i].M, t[i].N) >= 128)
+            return false;
+        work += tiles * steps;
     }
-    return true;
+    return work <= kGroupWork;
 }
 
 // t[0] is dX's product, t[1 .. n-1] are weight gradients of type w_dtype.
