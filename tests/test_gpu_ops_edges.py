@@ -1,0 +1,120 @@
+"""The feed-forward operators at the edges of their range: pre-activations whose
+square leaves fp32's range and infinite ones, on every kernel."""
+import pytest
+import torch
+
+from _ops_ref import ACTS, U, act, act_bound, product, rounding, slope_bound
+from test_gpu_ops import DT, FP8_INNER, clean, out, rand, tg, ws  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def agrees(got, want, tol, what):
+    """NaN and infinities where the definition has them, within tol elsewhere."""
+    got = got.double()
+    for name, a, b in (("NaN", got.isnan(), want.isnan()), ("inf", got == INF, want == INF), ("-inf", got == -INF, want == -INF)):
+        assert torch.equal(a, b), f"{what}: {int((a != b).sum())} values differ in being {name}"
+    r = torch.where(torch.isfinite(want) & (got != want), (got - want).abs() / tol.clamp(min=1e-300), torch.zeros_like(want))
+    assert float(r.max()) <= 1.0, f"{what}: {float(r.max()):.3g} of its bound"
+
+
+# few rows (one slice and two), the 64 and 128 tiles, the 256 tile, the generic tile
+EDGE_SHAPES = [(6, 136, 128), (23, 72, 136), (130, 201, 272), (1270, 1281, 72), (4090, 4097, 200), (50, 70, 33)]
+LARGE = (INF, -INF, 1e30, -1e30, 2e19, -2e19)  # rows 0 to 5 (fp16 holds the infinities alone)
+
+
+def edge_rows(M, N, K, t, seed):
+    """x whose first rows hold one of LARGE and zeros, and W."""
+    x, w = rand(M, K, t, seed), rand(N, K, t, seed + 1, K ** -0.5)
+    for r, v in enumerate(LARGE):
+        x[r] = 0.0
+        x[r, 0] = v if t != torch.float16 or abs(v) == INF else 6e4 * (1 if v > 0 else -1)
+    return x, w
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+def test_linear_large_and_infinite(tg, ws, name, dt, od):
+    for M, N, K in EDGE_SHAPES:
+        x, w = edge_rows(M, N, K, DT[dt], 1)
+        s, y = out(M, N, DT[od])
+        print(f"linear {M}x{N}x{K} {dt}->{od} {name}", flush=True)
+        tg.tg_linear(x, w, y, act=name, workspace=ws)
+        z, tol = product(x[:12], w)
+        v = act(name, z)[0]
+        agrees(y[:12], v, act_bound(name, z, v, tol) * (1 + 2.0 ** -7) + rounding(v, DT[od]), "y")
+        assert bool(torch.isfinite(y[6:]).all())
+        clean(s, M, N, "y")
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_glu_large_and_infinite(tg, ws, name, dt):
+    t = DT[dt]
+    for M, F, D in EDGE_SHAPES:
+        x, w = edge_rows(M, 2 * F, D, t, 1)
+        if t == torch.bfloat16:
+            w[F:, 0] *= 2.0 ** -100  # finite rows: an up projection of ordinary size beside the large gate
+        else:
+            w[:, 0] *= 2.0 ** -10
+        s, h = out(M, F, t)
+        print(f"glu {M}x{F}x{D} {dt} {name}", flush=True)
+        tg.tg_glu(x, w, h, act=name, workspace=ws)
+        p, b = product(x[:12], w)
+        g, u, eg, eu = p[:, :F], p[:, F:], b[:, :F], b[:, F:]
+        v = act(name, g)[0]
+        ev = act_bound(name, g, v, eg)
+        y = v * u
+        agrees(h[:12], y, (ev * u.abs() + (v.abs() + ev) * eu) + 2 * U * y.abs() + rounding(y, t), "h")
+        assert bool(torch.isfinite(h[6:]).all())
+        clean(s, M, F, "h")
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("M,N,K", [(6, 136, 128), (130, 208, 272), (1270, 1288, 272), (50, 70, 33)])
+def test_large_from_scales_and_bias(tg, ws, name, M, N, K):
+    """8-bit inputs with large scales, and an fp32 bias beside 16-bit inputs."""
+    x, w = rand(M, K, DT["fp8"], 1), rand(N, K, DT["fp8"], 2)
+    alpha = 2.0 ** 100
+    for od in ("bf16", "f32"):
+        y = out(M, N, DT[od])[1]
+        tg.tg_linear(x, w, y, act=name, scale_x=2.0 ** 50, scale_w=2.0 ** 50, workspace=ws)
+        z, tol = product(x, w, alpha, FP8_INNER)
+        v = act(name, z)[0]
+        agrees(y, v, act_bound(name, z, v, tol) * (1 + 2.0 ** -7) + rounding(v, DT[od]), f"y {od}")
+    F = N // 2
+    h = out(M, F, DT["bf16"])[1]
+    wide = w[:2 * F].float()
+    wide[F:] = 0.0
+    wide[F:, 0] = 2.0 ** -9  # (the squares of many g leave fp32's range, g * u stays in it)
+    w[:2 * F].copy_(wide)
+    tg.tg_glu(x, w[:2 * F], h, act=name, scale_x=2.0 ** 31, scale_w=2.0 ** 30, workspace=ws)
+    p, b = product(x, w[:2 * F], 2.0 ** 61, FP8_INNER)
+    g, u, eg, eu = p[:, :F], p[:, F:], b[:, :F], b[:, F:]
+    v = act(name, g)[0]
+    ev = act_bound(name, g, v, eg)
+    agrees(h, v * u, (ev * u.abs() + (v.abs() + ev) * eu) + 2 * U * (v * u).abs() + rounding(v * u, DT["bf16"]), "h")
+    x, w = rand(M, K, DT["f16"], 3), rand(N, K, DT["f16"], 4, K ** -0.5)
+    bias = torch.tensor([1e20, -1e20, 3e38, -3e38, 2e19, -2e19, 1.0, -1.0], device="cuda").repeat(N // 8 + 1)[:N].contiguous()
+    y = out(M, N, DT["f32"])[1]
+    tg.tg_linear(x, w, y, bias=bias, act=name, workspace=ws)
+    z, tol = product(x, w)
+    z = z + bias.double()
+    tol = tol + 4 * U * z.abs() + 2 * U * bias.double().abs()
+    v = act(name, z)[0]
+    agrees(y, v, act_bound(name, z, v, tol) * (1 + 2.0 ** -7) + rounding(v, DT["f32"]), "y, bias")
+
+
+@pytest.mark.parametrize("name", ACTS)
+def test_slopes_at_large_preactivations(tg, ws, name):
+    t = torch.bfloat16
+    M, N, K = 40, 64, 72
+    dy, x, w, z = rand(M, N, t, 1), rand(M, K, t, 2), rand(N, K, t, 3), rand(M, N, t, 4)
+    for r, v in enumerate(LARGE[2:]):
+        z[r] = v
+    dz, db = out(M, N, t)[1], torch.empty(N, device="cuda")
+    tg.tg_linear_backward(dy, x, w, dbias=db, preact=z, act=name, dz=dz, workspace=ws)
+    want = dy.double() * act(name, z.double())[1]
+    agrees(dy if name == "none" else dz, want, dy.double().abs() * slope_bound(name) + U * want.abs() + rounding(want, t), "dz")

@@ -81,13 +81,21 @@ __device__ __forceinline__ float normal_cdf(float x, float& e)
     return x < 0.0f ? q : 1.0f - q;
 }
 
+// x^2 as the logistic argument x (s1 + s3 x^2) takes it, held at 1e6: past
+// |x| = 1000 that argument is beyond +-1000 and s is 0 or 1 either way, while an
+// infinite square would make silu's s3 x^2 = 0 x^2 NaN.
+__device__ __forceinline__ float held_square(float x)
+{
+    return __builtin_fminf(x * x, 1e6f);
+}
+
 template <int KIND>
 __device__ __forceinline__ float act_value(float x, const EpiArgs& a)
 {
     if constexpr (KIND == AK_CLIP) {
         return x <= a.lo ? a.lo : x;  // (NaN stays)
     } else if constexpr (KIND == AK_SIGMOID) {
-        return x * sigmoid_f32(x * __builtin_fmaf(a.s3, x * x, a.s1));
+        return x * sigmoid_f32(x * __builtin_fmaf(a.s3, held_square(x), a.s1));
     } else {
         float e;
         return x * normal_cdf(x, e);
@@ -102,12 +110,11 @@ __device__ __forceinline__ float act_slope(float x, const EpiArgs& a, float& val
         value = x <= a.lo ? a.lo : x;
         return x <= a.lo ? a.slope_lo : 1.0f;
     } else if constexpr (KIND == AK_SIGMOID) {
-        // (past |x| = 1000 the factor s (1 - s) is zero: the square is held
-        // there so that it stays finite)
-        const float x2 = x * x, x2f = x2 > 1e6f ? 1e6f : x2;
-        const float s = sigmoid_f32(x * __builtin_fmaf(a.s3, x2f, a.s1));
+        // (past |x| = 1000 the factor s (1 - s) is zero too)
+        const float x2 = held_square(x);
+        const float s = sigmoid_f32(x * __builtin_fmaf(a.s3, x2, a.s1));
         value = x * s;
-        return __builtin_fmaf(value * (1.0f - s), __builtin_fmaf(3.0f * a.s3, x2f, a.s1), s);
+        return __builtin_fmaf(value * (1.0f - s), __builtin_fmaf(3.0f * a.s3, x2, a.s1), s);
     } else {
         float e;
         const float c = normal_cdf(x, e);
