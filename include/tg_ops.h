@@ -146,9 +146,9 @@ int64_t tg_glu_backward_workspace_bytes(tg_input in, int64_t M, int64_t F, int64
  * Squares and their sum are fp64, the factor is rounded to fp32 and each
  * product once more to the tensor's type.  A norm of infinity gives the
  * factor 0 (and NaN where a gradient is infinite), a NaN makes every output
- * NaN.  max_norm >= 0 (infinity: nothing is clipped) and eps >= 0, else
- * TG_ERR_INVALID_VALUE; norm + eps == 0 clips nothing.  The workspace is
- * required (when count > 0). */
+ * NaN.  max_norm >= 0 and eps >= 0, else TG_ERR_INVALID_VALUE.  Nothing is
+ * clipped with norm + eps == 0, nor with max_norm infinity, an infinite norm
+ * included.  The workspace is required (when count > 0 or norm is given). */
 tg_status tg_clip_grads(int64_t count, const void *const *grads, void *const *outs,
                         const int64_t *sizes, const int32_t *dtypes,
                         float max_norm, float eps, float *norm,

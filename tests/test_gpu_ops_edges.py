@@ -118,3 +118,24 @@ def test_slopes_at_large_preactivations(tg, ws, name):
     tg.tg_linear_backward(dy, x, w, dbias=db, preact=z, act=name, dz=dz, workspace=ws)
     want = dy.double() * act(name, z.double())[1]
     agrees(dy if name == "none" else dz, want, dy.double().abs() * slope_bound(name) + U * want.abs() + rounding(want, t), "dz")
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_infinite_max_norm_clips_nothing(tg, ws, in_place):
+    """Whatever the norm, infinity included; only a NaN still reaches every output."""
+    norm = torch.empty(1, device="cuda")
+    for bad in (0.0, 3e38, INF, -INF):
+        grads = [torch.randn(9001, device="cuda"), torch.randn(77, device="cuda", dtype=torch.bfloat16), torch.zeros(3, device="cuda")]
+        grads[0][8] = bad
+        before = [g.clone() for g in grads]
+        outs = grads if in_place else [torch.full_like(g, float("nan")) for g in grads]
+        tg.tg_clip_grads(grads, INF, out=None if in_place else outs, norm=norm, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(outs, before)), bad
+        assert (float(norm) == INF) == (abs(bad) == INF)
+    grads[0][8] = float("nan")
+    tg.tg_clip_grads(grads, INF, norm=norm, workspace=ws)
+    assert bool(norm.isnan().all()) and all(bool(g.isnan().all()) for g in grads)
+    a = torch.ones(5, device="cuda")  # a finite max_norm takes an infinite norm to the factor 0
+    a[2] = INF
+    tg.tg_clip_grads([a], 1e30, norm=norm, workspace=ws)
+    assert float(norm) == INF and bool(a[2].isnan()) and not a[:2].any() and not a[3:].any()

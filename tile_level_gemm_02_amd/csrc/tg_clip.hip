@@ -171,8 +171,9 @@ template <bool STREAM>
 __global__ __launch_bounds__(256) void clip_scale(ClipArgs p)
 {
     const double d = __builtin_sqrt(*p.total) + (double)p.eps;
-    const double c = d == 0.0 ? 1.0 : (double)p.max_norm / d;
-    const float coef = c > 1.0 ? 1.0f : (float)c;  // (NaN stays)
+    // (compared first: 0 / 0 and inf / inf clip nothing; a NaN norm fails the
+    // comparison and stays)
+    const float coef = d <= (double)p.max_norm ? 1.0f : (float)((double)p.max_norm / d);
     const uint32_t chunks = p.first[p.count];
     for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
         const uint32_t ch = chunks - 1u - i;
