@@ -1,0 +1,46 @@
+"""The Python side of the feed-forward operators (CPU only: nothing launches):
+what builds and runs without the native helper of tg_clip_grads."""
+import os
+
+import pytest
+import torch
+
+
+@pytest.fixture()
+def ops():
+    import tile_level_gemm_02_amd  # noqa: F401
+    from tile_level_gemm_02_amd import ops
+
+    return ops
+
+
+def test_the_products_do_without_the_helper(ops, monkeypatch, tmp_path):
+    monkeypatch.setattr(ops, "_fns", None)
+    monkeypatch.setattr(ops, "_bind", None)
+    monkeypatch.setattr(ops, "_BIND_PATH", str(tmp_path / "_tgbind.so"))
+    assert ops.tg_linear_workspace_bytes(torch.bfloat16, 1, 512, 8192) > 0
+    x, y = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):  # (of its checks: the tensors are not on the GPU)
+        ops.tg_linear(x, torch.zeros(8, 16, dtype=torch.bfloat16), y)
+    with pytest.raises(ImportError, match="tg_clip_grads"):
+        ops._load_bind()
+
+
+def test_the_helper_loads(ops):
+    ops._load_bind()
+    assert ops._clip_address and callable(ops._bind.clip_grads)
+
+
+def test_the_library_is_built_where_the_helper_cannot_be(monkeypatch, tmp_path):
+    from tile_level_gemm_02_amd import build as b
+
+    if not os.path.exists(b.HIPCC):
+        pytest.skip("hipcc not installed")
+    (tmp_path / "one.hip").write_text('extern "C" int one() { return 1; }\n')
+    (tmp_path / "bind.cpp").write_text("#error no headers\n")
+    for name, path in (("CSRC", tmp_path), ("BUILD", tmp_path / "o"), ("LIB", tmp_path / "lib.so"), ("BIND", tmp_path / "bind.so")):
+        monkeypatch.setattr(b, name, str(path))
+    (tmp_path / "bind.so").write_text("an older one")
+    with pytest.warns(RuntimeWarning, match="no headers"):
+        assert b.build() == str(tmp_path / "lib.so")
+    assert (tmp_path / "lib.so").exists() and not (tmp_path / "bind.so").exists()

@@ -36,23 +36,26 @@ EXPORTS = ("tg_linear", "tg_linear_workspace_bytes", "tg_linear_backward", "tg_l
 WORKSPACE_BYTES = (64 << 20) + (64 << 10)
 
 _fns = None
-_bind = None          # the native helper _tgbind.so
+_bind = None          # the native helper _tgbind.so of tg_clip_grads
 _clip_address = 0     # of tg_clip_grads in the loaded library
 _BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tgbind.so")
 
 
 def _load_bind():
+    """The helper, loaded by the first tg_clip_grads: the products do without it."""
+    global _bind, _clip_address
     if not os.path.exists(_BIND_PATH):
-        raise ImportError(f"{_BIND_PATH} is not built; run `python -m tile_level_gemm_02_amd.build`")
+        raise ImportError(f"{_BIND_PATH}, which tg_clip_grads needs, is not built; run `python -m tile_level_gemm_02_amd.build`")
     loader = importlib.machinery.ExtensionFileLoader("_tgbind", _BIND_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tgbind", loader))
     loader.exec_module(module)
-    return module
+    _clip_address = ctypes.cast(_lib().tg_clip_grads, ctypes.c_void_p).value
+    _bind = module
 
 
 def _lib():
     """The library with the argument types of these entry points set."""
-    global _fns, _bind, _clip_address
+    global _fns
     if _fns is None:
         lib = load()
         i64, vp, f32, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int
@@ -73,8 +76,6 @@ def _lib():
             fn.argtypes, fn.restype = [ci, i64, i64, i64], i64
         lib.tg_clip_grads_workspace_bytes.argtypes = [i64]
         lib.tg_clip_grads_workspace_bytes.restype = i64
-        _bind = _load_bind()
-        _clip_address = ctypes.cast(lib.tg_clip_grads, ctypes.c_void_p).value
         _fns = lib
     return _fns
 
@@ -339,8 +340,8 @@ def tg_clip_grads(grads, max_norm: float, out=None, norm=None, eps: float = 1e-6
         raise ValueError("tg_clip_grads needs a workspace")
     dev = _device(workspace, "the workspace")
     ps, ns = _ws(workspace, dev)
-    if _fns is None:
-        _lib()
+    if _bind is None:
+        _load_bind()
     code = _bind.clip_grads(_clip_address, grads if type(grads) is list else list(grads),
                             out if out is None or type(out) is list else list(out), max_norm, eps, norm, dev, ps, ns,
                             _current_stream(dev) if stream is None else _stream(stream))
