@@ -139,3 +139,36 @@ def test_infinite_max_norm_clips_nothing(tg, ws, in_place):
     a[2] = INF
     tg.tg_clip_grads([a], 1e30, norm=norm, workspace=ws)
     assert float(norm) == INF and bool(a[2].isnan()) and not a[:2].any() and not a[3:].any()
+
+
+def one_row(cols, t, seed):
+    """A row of a 16-bit matrix whose stride is off the 16-byte grid, NaN around it."""
+    s = torch.full((10, -(-cols // 16) * 16 + 1), float("nan"), device="cuda").to(t)
+    r = s[8:9, :cols]  # (starts on the grid)
+    r.copy_(rand(1, cols, t, seed))
+    return r
+
+
+@pytest.mark.parametrize("K", [8, 33, 64, 200, 4104])
+def test_one_token_with_any_stride(tg, ws, K):
+    """A token taken out of a matrix with unaligned rows, and contiguous rows of odd width."""
+    t, N = torch.bfloat16, 77
+    x, w = one_row(K, t, 1), rand(N, K, t, 2, K ** -0.5)
+    res, pre, y = (one_row(N, t, 3 + i) for i in range(3))
+    tg.tg_linear(x, w, y, act="silu", residual=res, preact=pre, workspace=ws)
+    z, tol = product(x, w)
+    v = act("silu", z)[0]
+    agrees(pre, z, tol + rounding(z, t), "preact")
+    agrees(y, v + res.double(), (act_bound("silu", z, v, tol) + 2 * U * (v + res.double()).abs()) * (1 + 2.0 ** -7) + rounding(v + res.double(), t), "y")
+    h = torch.empty(1, 38, device="cuda", dtype=t)
+    tg.tg_glu(x, w[:76], h, workspace=ws)
+    g, u, eg, eu = z[:, :38], z[:, 38:76], tol[:, :38], tol[:, 38:76]
+    v = act("silu", g)[0]
+    ev = act_bound("silu", g, v, eg)
+    agrees(h, v * u, (ev * u.abs() + (v.abs() + ev) * eu) + 2 * U * (v * u).abs() + rounding(v * u, t), "h")
+    dx, dw = one_row(K, t, 6), rand(N, K, t, 7)
+    tg.tg_linear_backward(y, x, w, dx=dx, dw=dw, workspace=ws)
+    p, b = product(y, w.t())
+    agrees(dx, p, b + rounding(p, t), "dx")
+    p = y.double().t() @ x.double()
+    agrees(dw, p, 4 * U * p.abs() + rounding(p, t), "dw")

@@ -44,3 +44,16 @@ def test_the_library_is_built_where_the_helper_cannot_be(monkeypatch, tmp_path):
     with pytest.warns(RuntimeWarning, match="no headers"):
         assert b.build() == str(tmp_path / "lib.so")
     assert (tmp_path / "lib.so").exists() and not (tmp_path / "bind.so").exists()
+
+
+def test_a_single_row_has_no_stride(ops):
+    """What stands between rows is not looked at where there is one row or none."""
+    for dtype in (torch.float16, torch.float32, torch.float8_e4m3fn):
+        wide = torch.zeros(3, 4104 + 13, dtype=dtype)
+        for rows in (0, 1):
+            for cols in (0, 1, 9, 4104):
+                t = wide[1:1 + rows, :cols]
+                ld = ops._mat(t, "x", rows, cols, (dtype,), -1)[1]
+                assert ld >= cols and ld * dtype.itemsize % 16 == 0, (dtype, rows, cols, ld)
+        assert ops._mat(wide[:2, :9], "x", 2, 9, (dtype,), -1)[1] == 4117  # (refused by the library)
+        assert ops._mat(torch.zeros(1, 9, dtype=dtype).expand(2, 9), "x", 2, 9, (dtype,), -1)[1] == 0

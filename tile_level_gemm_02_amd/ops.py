@@ -105,7 +105,8 @@ def _mat(t, name: str, rows: int, cols: int, dtypes, dev: int):
         raise ValueError(f"{name} must have unit stride along its last dimension")
     if t.get_device() != dev:
         raise ValueError(f"every tensor must be on the current GPU, {name} is on {t.device}")
-    return t.data_ptr(), (ld if rows > 1 or ld > cols else cols)
+    # one row has no second one: its stride is not looked at, an aligned one stands for it
+    return t.data_ptr(), (ld if rows > 1 else cols + 15 & -16)
 
 
 _NONE = (None, 0)
