@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from _ops_ref import ACTS, U, act, act_bound, product, rounding, slope_bound
-from test_gpu_ops import DT, FP8_INNER, clean, out, rand, tg, ws  # noqa: F401 (fixtures)
+from test_gpu_ops import DT, FP8_INNER, bwd_case, clean, glu_bwd_case, out, rand, tg, ws  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +172,15 @@ def test_one_token_with_any_stride(tg, ws, K):
     agrees(dx, p, b + rounding(p, t), "dx")
     p = y.double().t() @ x.double()
     agrees(dw, p, 4 * U * p.abs() + rounding(p, t), "dw")
+
+
+# weight gradients of one, two and three K steps that fill whole rounds of 256 tiles, the last ones with ragged edges
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 4096), (1, 8192, 2048), (100, 8192, 8192), (130, 8192, 8184), (40, 4088, 4096)])
+@pytest.mark.parametrize("dt,od", [("bf16", "bf16"), ("f16", "f32")])
+def test_linear_backward_whole_rounds(tg, ws, M, N, K, dt, od):
+    bwd_case(tg, M, N, K, dt, od, "none", ws)
+
+
+@pytest.mark.parametrize("M,F,D", [(16, 4096, 4096), (60, 4096, 4096), (130, 8192, 4096), (60, 4088, 4096)])
+def test_glu_backward_whole_rounds(tg, ws, M, F, D):
+    glu_bwd_case(tg, M, F, D, "bf16", "bf16", "silu", ws)

@@ -57,3 +57,21 @@ def test_a_single_row_has_no_stride(ops):
                 assert ld >= cols and ld * dtype.itemsize % 16 == 0, (dtype, rows, cols, ld)
         assert ops._mat(wide[:2, :9], "x", 2, 9, (dtype,), -1)[1] == 4117  # (refused by the library)
         assert ops._mat(torch.zeros(1, 9, dtype=dtype).expand(2, 9), "x", 2, 9, (dtype,), -1)[1] == 0
+
+
+def test_backward_query_follows_the_plan(ops):
+    """A pass whose weight gradient fills whole rounds of the chip runs product by product, and the query then reports
+    what its products need alone; a ragged neighbour is grouped, with partial tiles of its own."""
+    import tile_level_gemm_02_amd as tg
+
+    bf = torch.bfloat16
+
+    def alone(M, N, K):  # dX's product, and the column sums' partial sums (1 KiB per 256 columns and 32 rows)
+        blocks = (N + 255) // 256
+        splits = min(64, 1024 // blocks, (M + 31) // 32)
+        return max(tg.tg_gemm_ex_workspace_bytes(bf, M, K, N, b_layout="row"), 65536 + blocks * splits * 1024 if splits > 1 else 0)
+
+    for M, N, K in ((64, 8192, 8192), (16, 16384, 4096), (64, 8192, 2048)):
+        assert tg.tg_linear_backward_workspace_bytes(bf, M, N, K) == alone(M, N, K), (M, N, K)
+    for M, N, K in ((64, 8192, 9000), (200, 4096, 2048)):
+        assert tg.tg_linear_backward_workspace_bytes(bf, M, N, K) > alone(M, N, K), (M, N, K)

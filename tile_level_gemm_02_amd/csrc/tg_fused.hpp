@@ -414,14 +414,36 @@ GroupPlan plan_group(const TileArgs* t, int n, bool allow_split)
 
 // Whether a group takes these products: all on the NT kernel's grid, at most
 // kGroupWork tile steps together (128 for each of the 512 workgroups that run
-// at once), and none that fills half the chip with tiles of 256 over 32 steps
-// or more.  Grouped against one by one: 1024 x 6144 x 1536 (18 K steps)
-// 67 -> 64 us, 200 x 4096 x 2048 31 -> 26, gated 128 x 4096 x 2048 47 -> 41,
-// 1504 x 4000 x 1504 (45 K) 191 -> 158, 96 x 9000 x 3600 204 -> 147; what stays
-// out: 4096^3 (131 K) 260 -> 309, 7000 x 2048 x 1536 126 -> 135, for which the
-// 256 tile's fewer bytes per operation win.  (One that loses and is taken:
-// 64 x 8192 x 8192, 73 -> 85, a weight gradient of a single step.)
+// at once), none that fills half the chip with tiles of 256 over 32 steps or
+// more, and no weight gradient that by itself makes enough whole rounds of
+// 256 tiles of 256 (whole_rounds).  Grouped against one by one:
+// 1024 x 6144 x 1536 (18 K steps) 67 -> 64 us, 200 x 4096 x 2048 31 -> 26,
+// gated 128 x 4096 x 2048 48 -> 41, 1504 x 4000 x 1504 (45 K) 191 -> 158,
+// 96 x 9000 x 3600 207 -> 145; what stays out: 4096^3 (131 K) 260 -> 309,
+// 7000 x 2048 x 1536 126 -> 135, for which the 256 tile's fewer bytes per
+// operation win.
 constexpr int64_t kGroupWork = 65536;
+
+// Rounds of whole 256 tiles from which a weight gradient of `steps` K steps
+// keeps its pass out of the group: it leaves no unit idle for the others to
+// fill.  A single step (up to 64 rows) is all epilogue, which the larger tile
+// does better: one round in a linear pass, two in a gated one, whose three
+// products have more to share.  Bf16, one by one against grouped:
+// 64 x 8192 x 8192 72 against 80 us, 16 x 16384 x 4096 65 / 75, 64 x 8192 x
+// 4096 42 / 45, 64 x 8192 x 2048 27 / 30, gated 16 x 8192 x 4096 109 / 117,
+// 64 x 4096 x 4096 59 / 63, but (one round) 64 x 4096 x 2048 43 / 38.  Two
+// steps: 128 x 8192 x 8192 (four rounds) 92 / 89, 128 x 16384 x 4096 96 / 86,
+// gated 96 x 8192 x 8192 (eight) 241 / 262.  More: 256 x 8192 x 8192 113 / 118,
+// 160 x 4096 x 28672 158 / 185, gated 256 x 8192 x 4096 181 / 192, but (two
+// rounds) 256 x 8192 x 4096 63 / 60.  A short last round makes up for it in
+// the group's favour at every size (64 x 8192 x 9000 127 / 106, 64 x 6000 x
+// 6000 66 / 50, gated 64 x 7168 x 5120 135 / 125), and so do widths of a gated
+// block off the 64 grid, whose dh and dX run edge loops (64 x 8184 x 4096
+// 133 / 126, 8 x 8192 x 4088 131 / 122; linear 64 x 8184 x 8192 75 / 84).
+inline int64_t whole_rounds(int64_t steps, int n)
+{
+    return steps == 1 ? n - 1 : steps == 2 ? 8 : 4;
+}
 
 template <int E>
 bool group_takes(const TileArgs* t, int n)
@@ -435,7 +457,11 @@ bool group_takes(const TileArgs* t, int n)
         const int64_t tiles = n_tiles<kGroupTile, kGroupTile>(t[i].M, t[i].N), steps = (t[i].K + 63) / 64;
         if (tiles > kGroupWork || steps > kGroupWork)
             return false;
-        if (steps >= 32 && n_tiles<256, 256>(t[i].M, t[i].N) >= 128)
+        const int64_t tiles256 = n_tiles<256, 256>(t[i].M, t[i].N);
+        if (steps >= 32 && tiles256 >= 128)
+            return false;
+        if (i > 0 && tiles256 % 256 == 0 && tiles256 >= 256 * whole_rounds(steps, n) &&
+            (n == 2 || (t[0].K % 64 == 0 && t[0].N % 64 == 0)))
             return false;
         work += tiles * steps;
     }
