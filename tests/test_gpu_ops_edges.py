@@ -184,3 +184,24 @@ def test_linear_backward_whole_rounds(tg, ws, M, N, K, dt, od):
 @pytest.mark.parametrize("M,F,D", [(16, 4096, 4096), (60, 4096, 4096), (130, 8192, 4096), (60, 4088, 4096)])
 def test_glu_backward_whole_rounds(tg, ws, M, F, D):
     glu_bwd_case(tg, M, F, D, "bf16", "bf16", "silu", ws)
+
+
+@pytest.mark.parametrize("M", [8, 40, 200])
+def test_gelu_tail_holds_its_digits(tg, ws, M):
+    """gelu over its whole negative tail, relative to its value: the pre-activation is an fp32 bias beside a product
+    of zeros, so that it is exact.  Phi's fit is off by 1.5e-6 of it at most; beside that come the roundings of its
+    seven coefficients and steps, the reciprocal and the exponential (under 24 u together) and three roundings of the
+    exponent x^2/2.  Below -13 Phi leaves fp32's normal range."""
+    N = 4096
+    z = torch.linspace(-12.5, 12.5, N, device="cuda")
+    x, w = torch.zeros(M, 64, device="cuda", dtype=torch.float16), torch.zeros(N, 64, device="cuda", dtype=torch.float16)
+    want = act("gelu", z.double())[0]
+    rel = 1.6e-6 + U * (24 + 1.5 * z.double().square())
+    for od in (torch.float32, torch.float16):
+        y = torch.empty(M, N, device="cuda", dtype=od)
+        tg.tg_linear(x, w, y, bias=z, act="gelu", workspace=ws)
+        tol = rel * want.abs() + rounding(want, od)
+        agrees(y, want.expand(M, N), tol.expand(M, N), str(od))
+    x, w, y = x.bfloat16(), w.bfloat16(), torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+    tg.tg_linear(x, w, y, bias=z, act="gelu", workspace=ws)
+    agrees(y, want.expand(M, N), (rel * want.abs() + rounding(want, torch.bfloat16)).expand(M, N), "bf16")

@@ -16,12 +16,16 @@
 //   gelu_tanh x/2 (1 + tanh(c (x + 0.044715 x^3))), c = sqrt(2/pi): with
 //             (1 + tanh(a)) / 2 = s(2a) it is x * s(x (s1 + s3 x^2)) as silu
 //             is (s1 = 1, s3 = 0), so both run one code path;
-//   gelu      x * Phi(x), Phi(x) = erfc(-x / sqrt(2)) / 2, by Abramowitz and
-//             Stegun 7.1.26: erfc(v) = t (a1 + t (a2 + ...)) e^(-v^2) with
-//             t = 1 / (1 + 0.3275911 v) for v >= 0, off by at most 1.5e-7
-//             (a library erf takes both of its branches in a wave of mixed
-//             arguments, about three times the instructions); the derivative
-//             Phi(x) + x e^(-x^2/2) / sqrt(2 pi) uses the same exponential.
+//   gelu      x * Phi(x); for x <= 0 Phi(x) = t P(t) e^(-x^2/2) with
+//             t = 1 / (1 + c |x|) and a polynomial of seven terms, Phi(x) =
+//             1 - Phi(-x) above.  c and P were fitted to Phi e^(x^2/2) / t, a
+//             smooth function of t, by minimax over |x| <= 14: off by 0.6e-7 or by
+//             1.5e-6 of Phi, whichever is less, so that the tail keeps its
+//             digits (fp32 rounding of the exponent adds 1.5 u x^2, 1e-5 of
+//             the value at -10).  (A library erf takes both of its branches in
+//             a wave of mixed arguments, about three times the instructions.)
+//             The derivative Phi(x) + x e^(-x^2/2) / sqrt(2 pi) uses the same
+//             exponential.
 //
 // The paths (kinds) are told apart by a uniform branch outside the loops over
 // a tile's values, so that one kernel serves every activation.
@@ -70,14 +74,16 @@ __device__ __forceinline__ float sigmoid_f32(float t)
 // Phi(x) and e^(-x^2/2)
 __device__ __forceinline__ float normal_cdf(float x, float& e)
 {
-    const float v = __builtin_fabsf(x);  // (0.3275911 / sqrt(2) folded into t)
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.231641888f, v, 1.0f));
+    const float v = __builtin_fabsf(x);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.259861737f, v, 1.0f));
     e = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
-    float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-    q = __builtin_fmaf(t, q, 1.421413741f);
-    q = __builtin_fmaf(t, q, -0.284496736f);
-    q = __builtin_fmaf(t, q, 0.254829592f);
-    q = 0.5f * q * t * e;
+    float q = __builtin_fmaf(t, -0.0734351352f, 0.231094211f);
+    q = __builtin_fmaf(t, q, -0.10924048f);
+    q = __builtin_fmaf(t, q, 0.168300435f);
+    q = __builtin_fmaf(t, q, 0.0725724027f);
+    q = __builtin_fmaf(t, q, 0.107257396f);
+    q = __builtin_fmaf(t, q, 0.103451163f);
+    q = q * t * e;
     return x < 0.0f ? q : 1.0f - q;
 }
 
