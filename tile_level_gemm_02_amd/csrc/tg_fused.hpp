@@ -357,7 +357,8 @@ struct GroupArgs {
     uint32_t end[3];
 };
 
-constexpr int kGroupTile = 128, kGroupNH = 4, kGroupSteps = 16;
+constexpr int kGroupTile = 128, kGroupNH = 4, kGroupSteps = 16, kGroupPartials = 1000;
+static_assert(kGroupPartials / 2 * 4 <= kSplitMaxCounters, "a counter per wave of every split tile");
 
 template <int E, int OW>
 __global__ __launch_bounds__(256, 2) void gemm_group(GroupArgs g)
@@ -375,7 +376,9 @@ __global__ __launch_bounds__(256, 2) void gemm_group(GroupArgs g)
 
 // Split counts of the group's products, and the workspace they need: K split
 // so that no workgroup runs much longer than the whole group's share, within
-// the counters and 64 MiB of partial tiles.
+// 1000 partial tiles (62.5 MiB).  Split tiles are then 500 at most, and their
+// arrival counters, side by side as the plain GEMM's (kCounterStride), 2000 of
+// kSplitMaxCounters.
 struct GroupPlan {
     int64_t tiles[3], ws_bytes;
     int splits[3];
@@ -395,16 +398,15 @@ GroupPlan plan_group(const TileArgs* t, int n, bool allow_split)
     // 512 workgroups run at once; at least kGroupSteps steps each
     int64_t share = (work + 511) / 512;
     share = share < kGroupSteps ? kGroupSteps : share;
-    int64_t counters = 0, partials = 0;
+    int64_t partials = 0;
     for (int i = 0; i < n; ++i) {
         const int64_t kt = (t[i].K + KE - 1) / KE;
         int64_t s = allow_split ? kt / share : 1;
         s = s > 8 ? 8 : s;
-        while (s > 1 && (counters + p.tiles[i] * 4 > kSplitMaxCounters / 4 || partials + p.tiles[i] * s > 1000))
+        while (s > 1 && partials + p.tiles[i] * s > kGroupPartials)
             --s;
         if (s > 1) {
             p.splits[i] = (int)s;
-            counters += p.tiles[i] * 4;
             partials += p.tiles[i] * s;
         }
     }

@@ -56,11 +56,13 @@ struct FusedArgs : TileArgs {
 };
 
 // Words between the arrival counters of a K split.  The feed-forward
-// operators' calls give each counter a 64-byte line: arrivals at one line
+// operators' products give each counter a 64-byte line: arrivals at one line
 // queue up at the device-coherent level (1024 arrivals at 16 counters of one
-// line took 14 us).  A split's workgroups fit one round of the chip, so their
-// counters fit the workspace's 64 KiB: at most 128 tiles of 4 waves, or 128
-// last-round tiles of 8.
+// line took 14 us); the grouped launch of a backward pass, whose up to 500
+// split tiles of 4 waves would not fit the 64 KiB that way, and the plain GEMM
+// keep them side by side.  A product's split workgroups fit one round of the
+// chip, so their counters fit the workspace's 64 KiB: at most 128 tiles of 4
+// waves, or 128 last-round tiles of 8.
 template <class P, class Plain>
 constexpr uint32_t kCounterStride = std::is_same<P, Plain>::value ? 1u : 16u;
 
