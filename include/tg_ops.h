@@ -20,7 +20,10 @@
  * Speed: sums that run along a matrix's rows take fast kernels where the rows
  * fill whole 16-byte chunks (multiples of 8 elements, 16 for fp8), and so do
  * the column counts of the gradients' products; other sizes run a tile kernel
- * that is several times slower.
+ * that is several times slower.  So does a backward pass's product with a
+ * row-major weight (dX = dZ . W, dH = dY . Wd) that spans 2 GiB or nearly, which
+ * one buffer descriptor does not hold: at 24, 256 and 2048 tokens and K = 8192,
+ * 130560 rows of bf16 W take 0.38, 0.70 and 3.4 ms, 131072 rows 5.3, 5.3 and 32.
  *
  * workspace: as for tg_gemm_ex (256-byte aligned device memory, first 64 KiB
  * zero before first use and left zero, one per concurrently running call, or

@@ -205,3 +205,35 @@ def test_gelu_tail_holds_its_digits(tg, ws, M):
     x, w, y = x.bfloat16(), w.bfloat16(), torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
     tg.tg_linear(x, w, y, bias=z, act="gelu", workspace=ws)
     agrees(y, want.expand(M, N), (rel * want.abs() + rounding(want, torch.bfloat16)).expand(M, N), "bf16")
+
+
+def test_gradients_through_weights_past_2_gib(tg, ws):
+    """dX = dZ . W and dH = dY . Wd with row-major weights that span more than one buffer descriptor: another kernel
+    takes them."""
+    t = torch.bfloat16
+    M, N, K = 24, 131_080, 8200  # W: 2.15 GB
+    dy, x, w = rand(M, N, t, 1), rand(M, K, t, 2), rand(N, K, t, 3, K ** -0.5)
+    s, dx = out(M, K, t)
+    tg.tg_linear_backward(dy, x, w, dx=dx, workspace=ws)
+    want, size = 0.0, 0.0
+    for i in range(0, N, 16_384):
+        a, b = dy[:, i:i + 16_384].double(), w[i:i + 16_384].double()
+        want, size = want + a @ b, size + a.abs() @ b.abs()
+    agrees(dx, want, 2 * N * U * size + 4 * U * want.abs() + rounding(want, t), "dx")
+    clean(s, M, K, "dx")
+    del w, x
+    F, D = 131_080, 8200  # Wd: D x F
+    dy, wd, gu = rand(M, D, t, 4), rand(D, F, t, 5, F ** -0.5), rand(M, 2 * F, t, 6)
+    s, dgu = out(M, 2 * F, t)
+    w, x = torch.empty(2 * F, D, device="cuda", dtype=t), rand(M, D, t, 7)  # (not read: no dx, no dw)
+    tg.tg_glu_backward(dy, wd, x, w, gu, None, dgu, workspace=ws)
+    for i in range(0, F, 16_384):
+        j = min(F, i + 16_384)
+        g, u = gu[:, i:j].double(), gu[:, F + i:F + j].double()
+        dh, e = product(dy, wd[:, i:j].t())
+        v, slope = act("silu", g)
+        es, ev = slope_bound("silu"), act_bound("silu", g, v, torch.zeros_like(g))
+        dg, du = dh * u * slope, dh * v
+        agrees(dgu[:, i:j], dg, (e * slope.abs() + (dh.abs() + e) * es) * u.abs() + 3 * U * dg.abs() + rounding(dg, t), "dg")
+        agrees(dgu[:, F + i:F + j], du, e * v.abs() + (dh.abs() + e) * ev + U * du.abs() + rounding(du, t), "du")
+    clean(s, M, 2 * F, "dgate_up")
