@@ -434,7 +434,7 @@ constexpr int64_t kGroupWork = 65536;
 // 64 x 8192 x 8192 72 against 80 us, 16 x 16384 x 4096 65 / 75, 64 x 8192 x
 // 4096 42 / 45, 64 x 8192 x 2048 27 / 30, gated 16 x 8192 x 4096 109 / 117,
 // 64 x 4096 x 4096 59 / 63, but (one round) 64 x 4096 x 2048 43 / 38.  Two
-// steps: 128 x 8192 x 8192 (four rounds) 92 / 89, 128 x 16384 x 4096 96 / 86,
+// steps: 128 x 8192 x 8192 (four rounds) level, 128 x 16384 x 4096 95 / 82,
 // gated 96 x 8192 x 8192 (eight) 241 / 262.  More: 256 x 8192 x 8192 113 / 118,
 // 160 x 4096 x 28672 158 / 185, gated 256 x 8192 x 4096 181 / 192, but (two
 // rounds) 256 x 8192 x 4096 63 / 60.  A short last round makes up for it in
