@@ -314,3 +314,6 @@ def tg_dequant_w4(qweight, scales, W, K: int | None = None, group_size: int = 12
 from .ops import (tg_clip_grads, tg_clip_grads_workspace_bytes, tg_glu, tg_glu_backward,  # noqa: E402
                   tg_glu_backward_workspace_bytes, tg_glu_workspace_bytes, tg_linear, tg_linear_backward,
                   tg_linear_backward_workspace_bytes, tg_linear_workspace_bytes, tg_ops_workspace)
+from .int8 import tg_linear_i8, tg_linear_i8_workspace_bytes, tg_quantize_i8  # noqa: E402
+from .train import (tg_adamw, tg_linear_xent, tg_linear_xent_backward,  # noqa: E402
+                    tg_linear_xent_backward_workspace_bytes, tg_linear_xent_workspace_bytes)

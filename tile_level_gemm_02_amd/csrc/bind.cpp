@@ -1,7 +1,7 @@
-// Marshalling of tg_clip_grads for Python: reads the tensors of a list (their
-// types, sizes, devices and pointers) in C++.  Read one attribute at a time
-// from Python they take about 0.5 us each tensor, 72 us for 56 gradients with
-// their outputs, several times the kernels of a small call.
+// Marshalling of tg_clip_grads and tg_adamw for Python: reads the tensors of a
+// list (their types, sizes, devices and pointers) in C++.  Read one attribute at
+// a time from Python they take about 0.5 us each tensor, 72 us for 56 gradients
+// with their outputs, several times the kernels of a small call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "tg_ops.h"
+#include "tg_train.h"
 
 namespace {
 
@@ -97,7 +98,112 @@ PyObject* clip_grads(PyObject*, PyObject* args)
     }
 }
 
+// C type of a float tensor, or -1
+int dtype_of(const at::Tensor& t)
+{
+    const auto s = t.scalar_type();
+    return s == at::kFloat ? TG_F32 : s == at::kHalf ? TG_F16 : s == at::kBFloat16 ? TG_BF16 : -1;
+}
+
+// a tensor of one element of type `type` on GPU `dev`: its pointer, else null with an error set
+const void* scalar_on(PyObject* o, int64_t dev, at::ScalarType type, const char* what)
+{
+    const at::Tensor* t = contiguous_on(o, dev, what);
+    if (t == nullptr)
+        return nullptr;
+    if (t->scalar_type() != type || t->numel() != 1) {
+        PyErr_Format(PyExc_ValueError, "%s must be a %s tensor of one element", what, type == at::kLong ? "int64" : "float32");
+        return nullptr;
+    }
+    return t->data_ptr();
+}
+
+typedef tg_status (*adamw_fn)(int64_t, const tg_adamw_tensor*, int64_t, double, double, double, double, double, const float*, float,
+                              const int64_t*, const float*, void*);
+
+// adamw(function address, params, grads, exp_avg, exp_avg_sq, masters or None, their scales or None twice, step, lr, beta1,
+//       beta2, eps, weight decay, norm or None, max_norm, device index, stream) -> status
+PyObject* adamw(PyObject*, PyObject* args)
+{
+    unsigned long long fn, stream;
+    PyObject *list[7], *step_o, *lr_o, *norm;
+    double beta1, beta2, eps, decay;
+    float max_norm;
+    long long dev;
+    if (!PyArg_ParseTuple(args, "KO!O!O!O!OOOOOddddOfLK", &fn, &PyList_Type, &list[0], &PyList_Type, &list[1], &PyList_Type, &list[2],
+                          &PyList_Type, &list[3], &list[4], &list[5], &list[6], &step_o, &lr_o, &beta1, &beta2, &eps, &decay, &norm,
+                          &max_norm, &dev, &stream))
+        return nullptr;
+    const Py_ssize_t n = PyList_GET_SIZE(list[0]);
+    for (int k = 1; k < 7; ++k)
+        if (list[k] != Py_None && (!PyList_Check(list[k]) || PyList_GET_SIZE(list[k]) != n))
+            return refuse("every list must hold a tensor for each parameter");
+    if ((list[5] == Py_None) != (list[6] == Py_None))
+        return refuse("exp_avg_scales and exp_avg_sq_scales come together");
+    const bool eight = list[5] != Py_None;
+    try {
+        std::vector<tg_adamw_tensor> t(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            static const char* const names[7] = {"params", "grads", "exp_avg", "exp_avg_sq", "masters", "exp_avg_scales", "exp_avg_sq_scales"};
+            void* at[7] = {};
+            int type[2] = {};
+            int64_t size = 0;
+            for (int k = 0; k < 7; ++k) {
+                if (list[k] == Py_None)
+                    continue;
+                const at::Tensor* x = contiguous_on(PyList_GET_ITEM(list[k], i), dev, names[k]);
+                if (x == nullptr)
+                    return nullptr;
+                if (k < 2) {
+                    type[k] = dtype_of(*x);
+                    if (type[k] < 0)
+                        return refuse("params and grads must be float32, float16 or bfloat16");
+                } else if (x->scalar_type() != (eight && k < 4 ? at::kFloat8_e4m3fn : at::kFloat)) {
+                    PyErr_Format(PyExc_ValueError, "%s must be %s", names[k], eight && k < 4 ? "float8_e4m3fn beside scales" : "float32");
+                    return nullptr;
+                }
+                if (k == 0)
+                    size = x->numel();
+                if (x->numel() != (k < 5 ? size : (size + 255) / 256)) {
+                    PyErr_Format(PyExc_ValueError, "%s must match the parameter's size", names[k]);
+                    return nullptr;
+                }
+                at[k] = x->data_ptr();
+            }
+            if (at[4] != nullptr && type[0] == TG_F32)
+                return refuse("masters go with 16-bit params");
+            t[i] = tg_adamw_tensor{at[0], (float*)at[4], at[1], at[2], at[3], (float*)at[5], (float*)at[6], size, type[0], type[1]};
+        }
+        const void *pn = nullptr, *ps = nullptr, *pl = nullptr;
+        long long step = 1;
+        double lr = 0.0;
+        if (norm != Py_None && (pn = scalar_on(norm, dev, at::kFloat, "the norm")) == nullptr)
+            return nullptr;
+        if (THPVariable_Check(step_o)) {
+            if ((ps = scalar_on(step_o, dev, at::kLong, "step")) == nullptr)
+                return nullptr;
+        } else {
+            step = PyLong_AsLongLong(step_o);
+        }
+        if (THPVariable_Check(lr_o)) {
+            if ((pl = scalar_on(lr_o, dev, at::kFloat, "lr")) == nullptr)
+                return nullptr;
+        } else {
+            lr = PyFloat_AsDouble(lr_o);
+        }
+        if (PyErr_Occurred())
+            return nullptr;
+        const tg_status st = ((adamw_fn)(uintptr_t)fn)(n, t.data(), step, lr, beta1, beta2, eps, decay, (const float*)pn, max_norm,
+                                                       (const int64_t*)ps, (const float*)pl, (void*)(uintptr_t)stream);
+        return PyLong_FromLong((long)st);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 PyMethodDef methods[] = {{"clip_grads", clip_grads, METH_VARARGS, "Marshals a tg_clip_grads call; returns its status."},
+                         {"adamw", adamw, METH_VARARGS, "Marshals a tg_adamw call; returns its status."},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tgbind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,419 @@
+// tg_adamw: one AdamW step over many tensors (contract in include/tg_train.h).
+//
+//   m' = b1 m + (1 - b1) g;   v' = b2 v + (1 - b2) g^2
+//   w' = w (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v' / (1 - b2^t)) + eps)
+//
+// Bound by memory: every value is read once and written once (fp32 28 bytes a
+// value, bf16 weights and gradients with 8-bit states 10).  Tensors of one
+// combination of types share launches of up to kAdamTensors, whose
+// descriptors travel in the kernel arguments; workgroups walk the tensors'
+// chunks.  A lane takes V consecutive values in 16-byte pieces: 8 with fp32
+// states, 16 with 8-bit ones, where 16 lanes then hold a block of 256 and its
+// largest value is a reduction within a row of lanes.
+#include <math.h>
+
+#include "tg_abi.hpp"
+#include "tg_epilogue.hpp"
+#include "tg_train.h"
+
+namespace tg {
+
+constexpr int kAdamTensors = 48;       // descriptors per launch (under 4 KiB of kernel arguments)
+constexpr int64_t kAdamChunk = 4096;   // elements per chunk
+constexpr int64_t kAdamGrid = 2048;    // workgroups of a launch: 8 per compute unit
+constexpr int kAdamBlock = 256;        // elements per scale of 8-bit states
+constexpr float kE4m3Max = 448.0f, kE4m3Step = 0.001953125f;  // largest and smallest positive value
+constexpr float kAdamTiny = 7.888609052210118e-31f;           // 2^-100
+
+struct AdamHyper {
+    float b1, omb1, b2, omb2;  // omb: 1 - b
+    float decay, step_size, root, eps;
+    double lr, wd, beta1, beta2;  // where step or lr are in device memory
+    const int64_t* step_dev;
+    const float* lr_dev;
+    int64_t step;
+    const float* norm;
+    float max_norm;
+};
+
+struct AdamArgs {
+    void* p[kAdamTensors];
+    float* w[kAdamTensors];
+    const void* g[kAdamTensors];
+    void* m[kAdamTensors];
+    void* v[kAdamTensors];
+    float* sm[kAdamTensors];
+    float* sv[kAdamTensors];
+    int64_t n[kAdamTensors];
+    uint32_t first[kAdamTensors + 1];  // first chunk of each tensor; [count]: all
+    uint8_t aligned[kAdamTensors];     // every pointer on 16 bytes
+    int32_t count;
+    AdamHyper h;
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+// beta^t by squaring
+__host__ __device__ inline double beta_power(double beta, int64_t t)
+{
+    double r = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1)
+            r *= beta;
+        beta *= beta;
+    }
+    return r;
+}
+
+__host__ __device__ inline void adam_constants(AdamHyper& h, int64_t step, double lr)
+{
+    h.decay = (float)(1.0 - lr * h.wd);
+    h.step_size = (float)(lr / (1.0 - beta_power(h.beta1, step)));
+    h.root = (float)(1.0 / __builtin_sqrt(1.0 - beta_power(h.beta2, step)));
+}
+
+// V values of type O from element `e` on, `left` of them there; whole: all are,
+// on a 16-byte boundary.  STREAM: with the non-temporal hint.
+template <int O, int V, bool STREAM>
+__device__ __forceinline__ void load_values(const void* base, int64_t e, int left, bool whole, u32x4* q)
+{
+    constexpr int N = Piece<O>::N;
+    if (whole) {
+        const u32x4* src = (const u32x4*)((const typename OutInfo<O>::T*)base + e);
+#pragma unroll
+        for (int i = 0; i < V / N; ++i)
+            q[i] = STREAM ? __builtin_nontemporal_load(src + i) : src[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / N; ++i)
+            q[i] = load_piece<O>(base, e + i * N, left - i * N, false);
+    }
+}
+
+template <int O, int V>
+__device__ __forceinline__ void store_values(void* base, int64_t e, int left, bool whole, const float* v)
+{
+    constexpr int N = Piece<O>::N;
+#pragma unroll
+    for (int i = 0; i < V / N; ++i)
+        store_piece<O>(base, e + i * N, pack_piece<O>(v + i * N), left - i * N, whole);
+}
+
+// 16 bytes of e4m3
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_e4m3(const void* base, int64_t e, int left, bool whole)
+{
+    const uint8_t* src = (const uint8_t*)base + e;
+    if (whole)
+        return STREAM ? __builtin_nontemporal_load((const u32x4*)src) : *(const u32x4*)src;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < left)
+            w[i / 4] |= (uint32_t)src[i] << (8 * (i % 4));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+__device__ __forceinline__ void store_e4m3(void* base, int64_t e, int left, bool whole, u32x4 q)
+{
+    uint8_t* dst = (uint8_t*)base + e;
+    if (whole) {
+        store_nt((u32x4*)dst, q);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < left)
+            dst[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+}
+
+__device__ __forceinline__ void from_e4m3(u32x4 q, float scale, float* v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
+        v[4 * i] = lo[0] * scale;
+        v[4 * i + 1] = lo[1] * scale;
+        v[4 * i + 2] = hi[0] * scale;
+        v[4 * i + 3] = hi[1] * scale;
+    }
+}
+
+// largest of the 16 lanes of a row
+__device__ __forceinline__ float row_max(float v)
+{
+    // row_ror by 8, 4, 2, 1: every lane ends with all 16
+#define TG_ROW_MAX(ctrl) \
+    v = __builtin_fmaxf(v, bit_cast<float>(__builtin_amdgcn_mov_dpp(bit_cast<int>(v), ctrl, 0xF, 0xF, true)))
+    TG_ROW_MAX(0x128);
+    TG_ROW_MAX(0x124);
+    TG_ROW_MAX(0x122);
+    TG_ROW_MAX(0x121);
+#undef TG_ROW_MAX
+    return v;
+}
+
+// A block's values as e4m3 and a scale; LIFT: positive ones stay positive
+template <bool LIFT>
+__device__ __forceinline__ u32x4 to_e4m3(const float* v, float& scale)
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = __builtin_fmaxf(top, LIFT ? v[i] : __builtin_fabsf(v[i]));
+    top = row_max(top);
+    top = top < kAdamTiny ? 0.0f : top;
+    const float inv = top > 0.0f ? kE4m3Max / top : 0.0f;
+    scale = top * (1.0f / kE4m3Max);
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] = v[4 * i + e] * inv;
+            if (LIFT)
+                s[e] = s[e] > 0.0f ? __builtin_fmaxf(s[e], kE4m3Step) : s[e];
+        }
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], w, true);
+        q[i] = (uint32_t)w;
+    }
+    return q;
+}
+
+__device__ __forceinline__ int adam_tensor(const AdamArgs& p, uint32_t c)
+{
+    int lo = 0, hi = p.count;  // first[lo] <= c < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (p.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// P: type of the weights, G: of the gradients; MASTER: fp32 weights beside
+// them; EIGHT: 8-bit states
+template <int P, int G, bool MASTER, bool EIGHT, bool STREAM>
+__global__ __launch_bounds__(256) void adamw_step(AdamArgs a)
+{
+    static_assert(!MASTER || P != O_F32, "masters of 16-bit weights");
+    constexpr int V = EIGHT ? 16 : 8, WT = MASTER ? (int)O_F32 : P;
+    AdamHyper h = a.h;
+    float coef = 1.0f;
+    if (h.norm != nullptr) {
+        const float norm = *h.norm, d = norm + 1e-6f;
+        if (!(__builtin_fabsf(norm) < INFINITY))
+            return;
+        coef = d <= h.max_norm ? 1.0f : h.max_norm / d;
+    }
+    if (h.step_dev != nullptr || h.lr_dev != nullptr)
+        adam_constants(h, h.step_dev != nullptr ? *h.step_dev : h.step, h.lr_dev != nullptr ? (double)*h.lr_dev : h.lr);
+    const uint32_t chunks = a.first[a.count], tid = threadIdx.x;
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int t = adam_tensor(a, c);
+        const int64_t c0 = (int64_t)(c - a.first[t]) * kAdamChunk, n = a.n[t];
+        const bool aligned = a.aligned[t] != 0;
+#pragma unroll
+        for (int k = 0; k < (int)kAdamChunk / (256 * V); ++k) {
+            const int64_t e0 = c0 + (int64_t)k * 256 * V + tid * V, rest = n - e0;
+            const int left = rest >= V ? V : rest > 0 ? (int)rest : 0;
+            const bool whole = aligned && left == V;
+            u32x4 gq[V / Piece<G>::N], wq[V / Piece<WT>::N], mq[EIGHT ? 1 : V / 4], vq[EIGHT ? 1 : V / 4];
+            float w[V], m[V], v[V], r[V];
+            if (left > 0) {
+                load_values<G, V, STREAM>(a.g[t], e0, left, whole, gq);
+                load_values<WT, V, STREAM>(MASTER ? (const void*)a.w[t] : a.p[t], e0, left, whole, wq);
+                if constexpr (EIGHT) {
+                    mq[0] = load_e4m3<STREAM>(a.m[t], e0, left, whole);
+                    vq[0] = load_e4m3<STREAM>(a.v[t], e0, left, whole);
+                    from_e4m3(mq[0], a.sm[t][e0 / kAdamBlock], m);
+                    from_e4m3(vq[0], a.sv[t][e0 / kAdamBlock], v);
+                } else {
+                    load_values<O_F32, V, STREAM>(a.m[t], e0, left, whole, mq);
+                    load_values<O_F32, V, STREAM>(a.v[t], e0, left, whole, vq);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    w[i] = m[i] = v[i] = r[i] = 0.0f;
+            }
+            if (left > 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float g = piece_value<G>(gq[i / Piece<G>::N], i % Piece<G>::N) * coef;
+                    const float w0 = piece_value<WT>(wq[i / Piece<WT>::N], i % Piece<WT>::N);
+                    const float m0 = EIGHT ? m[i] : piece_value<O_F32>(mq[EIGHT ? 0 : i / 4], i % 4);
+                    const float v0 = EIGHT ? v[i] * v[i] : piece_value<O_F32>(vq[EIGHT ? 0 : i / 4], i % 4);
+                    m[i] = m0 * h.b1 + g * h.omb1;
+                    v[i] = v0 * h.b2 + g * h.omb2 * g;
+                    r[i] = __builtin_amdgcn_sqrtf(v[i]);
+                    w[i] = w0 * h.decay - m[i] * __builtin_amdgcn_rcpf(r[i] * h.root + h.eps) * h.step_size;
+                }
+                if constexpr (EIGHT) {
+                    // (values past the tensor's end: out of the block's largest)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (i >= left)
+                            m[i] = r[i] = 0.0f;
+                }
+                store_values<P, V>(a.p[t], e0, left, whole, w);
+                if constexpr (MASTER)
+                    store_values<O_F32, V>(a.w[t], e0, left, whole, w);
+            }
+            if constexpr (EIGHT) {
+                // (every lane of the row takes part)
+                float sm, sv;
+                const u32x4 qm = to_e4m3<false>(m, sm), qv = to_e4m3<true>(r, sv);
+                if (left > 0) {
+                    store_e4m3(a.m[t], e0, left, whole, qm);
+                    store_e4m3(a.v[t], e0, left, whole, qv);
+                    if (e0 % kAdamBlock == 0) {
+                        a.sm[t][e0 / kAdamBlock] = sm;
+                        a.sv[t][e0 / kAdamBlock] = sv;
+                    }
+                }
+            } else if (left > 0) {
+                store_values<O_F32, V>(a.m[t], e0, left, whole, m);
+                store_values<O_F32, V>(a.v[t], e0, left, whole, v);
+            }
+        }
+    }
+}
+
+template <int P, int G, bool MASTER, bool EIGHT>
+static void adam_launch(const AdamArgs& a, uint32_t grid, bool stream, hipStream_t s)
+{
+    if (stream)
+        hipLaunchKernelGGL((adamw_step<P, G, MASTER, EIGHT, true>), dim3(grid), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((adamw_step<P, G, MASTER, EIGHT, false>), dim3(grid), dim3(256), 0, s, a);
+}
+
+template <int P, int G>
+static void adam_launch_pg(bool master, bool eight, const AdamArgs& a, uint32_t grid, bool stream, hipStream_t s)
+{
+    if (master && P != O_F32)
+        eight ? adam_launch<P, G, P != O_F32, true>(a, grid, stream, s) : adam_launch<P, G, P != O_F32, false>(a, grid, stream, s);
+    else
+        eight ? adam_launch<P, G, false, true>(a, grid, stream, s) : adam_launch<P, G, false, false>(a, grid, stream, s);
+}
+
+template <int P>
+static void adam_launch_p(int g, bool master, bool eight, const AdamArgs& a, uint32_t grid, bool stream, hipStream_t s)
+{
+    switch (g) {
+    case TG_F32: adam_launch_pg<P, O_F32>(master, eight, a, grid, stream, s); break;
+    case TG_F16: adam_launch_pg<P, O_F16>(master, eight, a, grid, stream, s); break;
+    default: adam_launch_pg<P, O_BF16>(master, eight, a, grid, stream, s); break;
+    }
+}
+
+static bool dtype_ok(int t) { return t == TG_F32 || t == TG_F16 || t == TG_BF16; }
+static uintptr_t elem_mask(int t) { return t == TG_F32 ? 3u : 1u; }
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" tg_status tg_adamw(int64_t count, const tg_adamw_tensor* tensors, int64_t step, double lr, double beta1, double beta2,
+                              double eps, double weight_decay, const float* norm, float max_norm, const int64_t* step_dev,
+                              const float* lr_dev, void* stream)
+{
+    if (count < 0 || (count > 0 && tensors == nullptr) || (step_dev == nullptr && step < 1) ||
+        (lr_dev == nullptr && !__builtin_isfinite(lr)) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !(eps >= 0.0) || __builtin_isinf(eps) || !__builtin_isfinite(weight_decay) || !(max_norm >= 0.0f))
+        return TG_ERR_INVALID_VALUE;
+    if (((uintptr_t)norm & 3u) || ((uintptr_t)lr_dev & 3u) || ((uintptr_t)step_dev & 7u))
+        return TG_ERR_MISALIGNED;
+    int64_t bytes = 0;
+    bool eight = false, fp32 = false;
+    for (int64_t i = 0; i < count; ++i) {
+        const tg_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || !dtype_ok(t.p_dtype) || !dtype_ok(t.g_dtype))
+            return TG_ERR_INVALID_VALUE;
+        if (t.n == 0)
+            continue;
+        if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr ||
+            (t.exp_avg_scale == nullptr) != (t.exp_avg_sq_scale == nullptr) || (t.master != nullptr && t.p_dtype == TG_F32))
+            return TG_ERR_INVALID_VALUE;
+        const bool e = t.exp_avg_scale != nullptr;
+        (e ? eight : fp32) = true;
+        const uintptr_t states = e ? 0u : 3u;
+        if (((uintptr_t)t.param & elem_mask(t.p_dtype)) || ((uintptr_t)t.grad & elem_mask(t.g_dtype)) || ((uintptr_t)t.master & 3u) ||
+            ((uintptr_t)t.exp_avg & states) || ((uintptr_t)t.exp_avg_sq & states) || ((uintptr_t)t.exp_avg_scale & 3u) ||
+            ((uintptr_t)t.exp_avg_sq_scale & 3u))
+            return TG_ERR_MISALIGNED;
+        if (t.n > (int64_t)1 << 40)
+            return TG_ERR_NOT_SUPPORTED;
+        bytes += t.n * ((t.p_dtype == TG_F32 ? 4 : 2) + (t.g_dtype == TG_F32 ? 4 : 2) + (t.master != nullptr ? 4 : 0) + (e ? 2 : 8));
+    }
+    if (eight && fp32)
+        return TG_ERR_INVALID_VALUE;
+
+    AdamArgs a;
+    AdamHyper& h = a.h;
+    h.b1 = (float)beta1;
+    h.omb1 = (float)(1.0 - beta1);
+    h.b2 = (float)beta2;
+    h.omb2 = (float)(1.0 - beta2);
+    h.eps = (float)eps;
+    h.lr = lr;
+    h.wd = weight_decay;
+    h.beta1 = beta1;
+    h.beta2 = beta2;
+    h.step = step;
+    h.step_dev = step_dev;
+    h.lr_dev = lr_dev;
+    h.norm = norm;
+    h.max_norm = max_norm;
+    h.decay = h.step_size = h.root = 0.0f;
+    if (step_dev == nullptr && lr_dev == nullptr)
+        adam_constants(h, step, lr);
+    // one combination of types after another, up to kAdamTensors tensors a launch
+    for (int kind = 0; kind < 18; ++kind) {  // (masters of fp32 weights: none)
+        const int p = kind / 6, g = kind / 2 % 3;
+        const bool master = kind % 2 != 0;
+        for (int64_t i = 0; i < count;) {
+            int64_t chunks = 0;
+            a.count = 0;
+            for (; i < count && a.count < kAdamTensors; ++i) {
+                const tg_adamw_tensor& t = tensors[i];
+                if (t.n == 0 || t.p_dtype != p || t.g_dtype != g || (t.master != nullptr) != master)
+                    continue;
+                const int64_t c = (t.n + kAdamChunk - 1) / kAdamChunk;
+                if (chunks + c > 0xFFFFFFFF)
+                    break;
+                const int k = a.count++;
+                a.p[k] = t.param;
+                a.w[k] = t.master;
+                a.g[k] = t.grad;
+                a.m[k] = t.exp_avg;
+                a.v[k] = t.exp_avg_sq;
+                a.sm[k] = t.exp_avg_scale;
+                a.sv[k] = t.exp_avg_sq_scale;
+                a.n[k] = t.n;
+                a.first[k] = (uint32_t)chunks;
+                a.aligned[k] = (((uintptr_t)t.param | (uintptr_t)t.master | (uintptr_t)t.grad | (uintptr_t)t.exp_avg |
+                                 (uintptr_t)t.exp_avg_sq) & 15u) == 0;
+                chunks += c;
+            }
+            if (a.count == 0)
+                continue;
+            a.first[a.count] = (uint32_t)chunks;
+            const uint32_t grid = (uint32_t)(chunks < kAdamGrid ? chunks : kAdamGrid);
+            // (what exceeds the 256 MB Infinity Cache is read with the non-temporal hint)
+            const bool streamed = bytes > (int64_t)256 << 20;
+            switch (p) {
+            case TG_F32: adam_launch_p<O_F32>(g, master, eight, a, grid, streamed, (hipStream_t)stream); break;
+            case TG_F16: adam_launch_p<O_F16>(g, master, eight, a, grid, streamed, (hipStream_t)stream); break;
+            default: adam_launch_p<O_BF16>(g, master, eight, a, grid, streamed, (hipStream_t)stream); break;
+            }
+            if (hipGetLastError() != hipSuccess)
+                return TG_ERR_LAUNCH;
+        }
+    }
+    return TG_OK;
+}

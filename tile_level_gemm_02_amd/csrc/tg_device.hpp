@@ -26,9 +26,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // element type of A and B
-enum Elem : int { E_F16 = 0, E_BF16 = 1, E_FP8 = 2 };
+enum Elem : int { E_F16 = 0, E_BF16 = 1, E_FP8 = 2, E_I8 = 3 };
 // output type of C
 enum Out : int { O_F32 = 0, O_F16 = 1, O_BF16 = 2 };
 
@@ -36,6 +38,7 @@ template <int E> struct ElemInfo;
 template <> struct ElemInfo<E_F16> { static constexpr int bytes = 2; };
 template <> struct ElemInfo<E_BF16> { static constexpr int bytes = 2; };
 template <> struct ElemInfo<E_FP8> { static constexpr int bytes = 1; };
+template <> struct ElemInfo<E_I8> { static constexpr int bytes = 1; };
 
 template <typename T, typename F> __device__ __forceinline__ T bit_cast(F f)
 {
@@ -72,6 +75,50 @@ template <> struct Mfma32<E_FP8> {
         return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
     }
 };
+
+// int8: kstep 32, 16 elements per lane.  The int32 sums travel as the bits of
+// the fp32 registers that every kernel here holds its accumulators in (acc_add
+// and acc_value know them apart).
+template <> struct Mfma32<E_I8> {
+    typedef u32x4 frag;
+    __device__ __forceinline__ static f32x16 run(frag a, frag b, f32x16 c)
+    {
+        return bit_cast<f32x16>(__builtin_amdgcn_mfma_i32_32x32x32_i8(bit_cast<i32x4>(a), bit_cast<i32x4>(b), bit_cast<i32x16>(c), 0, 0, 0));
+    }
+};
+
+// sum of two accumulated values, and an accumulated value as fp32
+template <int E> __device__ __forceinline__ float acc_add(float a, float b)
+{
+    if constexpr (E == E_I8)
+        return bit_cast<float>(bit_cast<int>(a) + bit_cast<int>(b));
+    else
+        return a + b;
+}
+
+template <int E> __device__ __forceinline__ f32x4 acc_add(f32x4 a, f32x4 b)
+{
+    if constexpr (E == E_I8)
+        return bit_cast<f32x4>(bit_cast<i32x4>(a) + bit_cast<i32x4>(b));
+    else
+        return a + b;
+}
+
+template <int E> __device__ __forceinline__ float acc_value(float a)
+{
+    if constexpr (E == E_I8)
+        return (float)bit_cast<int>(a);
+    else
+        return a;
+}
+
+template <int E> __device__ __forceinline__ f32x4 acc_value(f32x4 a)
+{
+    if constexpr (E == E_I8)
+        return f32x4{acc_value<E>(a[0]), acc_value<E>(a[1]), acc_value<E>(a[2]), acc_value<E>(a[3])};
+    else
+        return a;
+}
 
 // Wait states between the last MFMA of a kernel and the first instruction that
 // reads its accumulators.  A 16-pass MFMA (the fp8 32x32x64 form) needs 18

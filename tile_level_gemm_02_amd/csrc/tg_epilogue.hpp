@@ -7,6 +7,8 @@
 //                 32 (see gemm_nt);  C = act(gate) * up;  both kept if asked
 //   EPI_GLU_BWD : acc is dh, the gradient of h = act(g) * u;
 //                 dg = dh * u * act'(g),  du = dh * act(g)
+//   EPI_OWN     : the arguments' type brings its own (P::finish, and
+//                 P::finish_quad for the skinny kernel)
 //
 // All arithmetic is fp32, on the unrounded accumulator; each stored value is
 // rounded once.  The activations:
@@ -47,7 +49,7 @@
 
 namespace tg {
 
-enum Epi : int { EPI_STORE = 0, EPI_LINEAR = 1, EPI_GLU = 2, EPI_GLU_BWD = 3 };
+enum Epi : int { EPI_STORE = 0, EPI_LINEAR = 1, EPI_GLU = 2, EPI_GLU_BWD = 3, EPI_OWN = 4 };
 
 // code paths of the activations
 enum ActKind : int { AK_CLIP = 0, AK_SIGMOID = 1, AK_ERF = 2 };
@@ -348,6 +350,62 @@ __device__ __forceinline__ void glu_epilogue(uint8_t* ep, uint32_t lane, int64_t
                                          [&](int i, int q) __attribute__((always_inline)) {
                                              return get(i, (q / QB * 2 + 1) * QB + q % QB);
                                          });
+    }
+}
+
+// The way that epilogues of their own (EPI_OWN) take their rows: the fp32
+// values go through LDS (PBY bytes of this wave's own) in passes and come back
+// as rows, VC consecutive columns per lane, the lane's first column being
+// VC (lane % (WC / VC)) in every row.  load(op, row) is called for each of a
+// pass's rows ahead of its staging, use(op, row, values) behind it.
+template <int VC, class Op, int RBK, int WR, int WC, int PBY, class Get, class Load, class Use>
+__device__ __forceinline__ void staged_rows(uint8_t* ep, uint32_t lane, int64_t row0, Get get, Load load, Use use)
+{
+    constexpr int G = 64 / RBK, NQ = WC / (4 * G);
+    constexpr int LPR = WC / VC, RPT = 64 / LPR;  // lanes per row, rows per instruction
+    constexpr int OB = WC * 4, NCH = OB / 16;
+    constexpr int PR = PBY / OB >= WR ? WR : (PBY / OB >= WR / 2 ? WR / 2 : WR / 4);
+    constexpr int NTI = PR / RPT;
+    static_assert(PR % RBK == 0 && WR % PR == 0 && PR % RPT == 0 && 64 % LPR == 0 && PR * OB <= PBY, "staging passes");
+    const uint32_t ec = lane % LPR, er = lane / LPR;
+    auto run_pass = [&](auto pass_c) __attribute__((always_inline)) {
+        constexpr int pass = decltype(pass_c)::value;
+        const int64_t prow = row0 + pass * PR + er;
+        Op op[NTI];
+#pragma unroll
+        for (int t = 0; t < NTI; ++t)
+            load(op[t], prow + t * RPT);
+#pragma unroll
+        for (int ii = 0; ii < PR / RBK; ++ii) {
+            const uint32_t r = ii * RBK + lane % RBK;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const uint32_t c = q * G + lane / RBK;  // 16-byte chunk of the quad
+                *(f32x4*)(ep + r * OB + ((c ^ (r % NCH)) << 4)) = get(pass * (PR / RBK) + ii, q);
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's staging writes done
+#pragma unroll
+        for (int t = 0; t < NTI; ++t) {
+            const uint32_t r = t * RPT + er;
+            float z[VC];
+#pragma unroll
+            for (int h = 0; h < VC / 4; ++h) {
+                const f32x4 q = bit_cast<f32x4>(lds128(ep, r * OB + (((ec * (VC / 4) + h) ^ (r % NCH)) << 4)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[4 * h + e] = q[e];
+            }
+            use(op[t], prow + t * RPT, z);
+        }
+    };
+    // (a call per pass, not a loop: the accumulator must be indexed by constants)
+    run_pass(std::integral_constant<int, 0>{});
+    if constexpr (WR / PR >= 2)
+        run_pass(std::integral_constant<int, 1>{});
+    if constexpr (WR / PR == 4) {
+        run_pass(std::integral_constant<int, 2>{});
+        run_pass(std::integral_constant<int, 3>{});
     }
 }
 

@@ -1,6 +1,6 @@
 // The 256 x 256 tile of the feed-forward operators' products, for 16-bit
 // inputs (A: M x K rows, or its transpose, K x M rows; B: N x K rows, or K x N
-// rows; any fused epilogue).  The staging, the ring of LDS half-stages, the
+// rows; any fused epilogue) and int8 (N x K rows: the same bytes, twice the k).  The staging, the ring of LDS half-stages, the
 // tile walk and the K split are gemm_nt's; what differs is the matrix
 // instruction and the loop around it.
 //
@@ -32,11 +32,11 @@ struct FxArgs : TileArgs {
 template <int E, int O, int NH, int AL, int BL, int EPI, class P>
 __global__ __launch_bounds__(512) void gemm_fx(P p)
 {
-    static_assert(ElemInfo<E>::bytes == 2, "16-bit inputs");
+    static_assert(ElemInfo<E>::bytes == 2 || (E == E_I8 && AL == A_KCONTIG && BL == B_KCONTIG), "16-bit inputs, or rows of int8");
     constexpr bool GLU = EPI == EPI_GLU;
     constexpr int BM = 256, BN = 256, WM = 2, WN = 4, NW = 8;
     constexpr int BNO = GLU ? BN / 2 : BN;  // output columns per tile
-    constexpr int EB = 2, CE = 8, RB = 128, KE = RB / EB, CH = 8;
+    constexpr int EB = ElemInfo<E>::bytes, CE = 16 / EB, RB = 128, KE = RB / EB, CH = 8;
     constexpr int AI = 4, BI = 4;  // copy instructions per wave and half-stage
     constexpr uint32_t HALF = 256 * RB;
     constexpr int LDS_BYTES = NH * (int)HALF;
@@ -335,16 +335,18 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
                     v[b] = splitk_load(src, (b0 + b) / 4, b % 4, lane);
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
-                    acc[(b0 + b) / 4][b % 4] = q == 0u ? v[b] : acc[(b0 + b) / 4][b % 4] + v[b];
+                    acc[(b0 + b) / 4][b % 4] = q == 0u ? v[b] : acc_add<E>(acc[(b0 + b) / 4][b % 4], v[b]);
             }
         }
     }
 
     // ---- epilogue
     const int64_t row0 = m0 + wm * 128, col0 = n0 + wn * (BNO / WN);
-    auto quad = [&](int i, int q) __attribute__((always_inline)) -> f32x4 { return acc[i][q]; };
+    auto quad = [&](int i, int q) __attribute__((always_inline)) -> f32x4 { return acc_value<E>(acc[i][q]); };
     uint8_t* const ep = lds + wave * (LDS_BYTES / NW);
-    if constexpr (GLU)
+    if constexpr (EPI == EPI_OWN)
+        p.template finish<16, 128, 64, LDS_BYTES / NW>(ep, lane, row0, col0, quad);
+    else if constexpr (GLU)
         glu_epilogue<O, 16, 128, 64>(ep, lane, row0, col0, M, N, p.C, p.ldc, p.e, quad);
     else if constexpr (EPI == EPI_STORE && O != O_F32)
         store_rows16<O, 16, 128, 64>(ep, lane, row0, col0, M, N, p.C, p.ldc, 0, true, quad);

@@ -683,7 +683,7 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     acc[b / TN][b % TN][4 * g + e] =
-                                        q == 0u ? x[e] : acc[b / TN][b % TN][4 * g + e] + x[e];
+                                        q == 0u ? x[e] : acc_add<E>(acc[b / TN][b % TN][4 * g + e], x[e]);
                             }
                     }
                 }
@@ -707,7 +707,7 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
                         for (int g = 0; g < 4; ++g)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                acc[i][j][4 * g + e] = q == 0u ? v[bb][g][e] : acc[i][j][4 * g + e] + v[bb][g][e];
+                                acc[i][j][4 * g + e] = q == 0u ? v[bb][g][e] : acc_add<E>(acc[i][j][4 * g + e], v[bb][g][e]);
                     }
                 }
             }
@@ -718,7 +718,7 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
     constexpr int WR = BM / WM, WC = BN / WN;  // this wave's sub-tile
     const int64_t wrow0 = m0 + wm * WR, wcol0 = n0 + wn * (BNO / WN);
     auto out_val = [&](int i, int j, int v) __attribute__((always_inline)) -> float {
-        float x = acc[i][j][v];
+        float x = acc_value<E>(acc[i][j][v]);
         if constexpr (E == E_FP8)
             x *= p.alpha;
         return x;
@@ -728,7 +728,9 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
         return f32x4{out_val(i, j, v), out_val(i, j, v + 1), out_val(i, j, v + 2), out_val(i, j, v + 3)};
     };
     (void)quad;
-    if constexpr (EPI == EPI_GLU) {
+    if constexpr (EPI == EPI_OWN) {
+        p.template finish<32, WR, WC, LDS_BYTES / NW>(lds + wave * (LDS_BYTES / NW), lane, wrow0, wcol0, quad);
+    } else if constexpr (EPI == EPI_GLU) {
         static_assert(NW * WR * WC <= LDS_BYTES, "epilogue staging");
         glu_epilogue<O, 32, WR, WC>(lds + wave * (WR * WC), lane, wrow0, wcol0, M, N, p.C, p.ldc, p.e, quad);
     } else if constexpr (EPI != EPI_STORE) {

@@ -224,7 +224,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
     for (int g = 0; g < CG; ++g)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            red[((wave * CG + g) * 4 + v) * 64 + lane] = acc[g][0][v] + acc[g][1][v];
+            red[((wave * CG + g) * 4 + v) * 64 + lane] = acc_add<E>(acc[g][0][v], acc[g][1][v]);
     __syncthreads();
     if constexpr (EPI != EPI_STORE) {
         if (wave < (uint32_t)(GLU ? 1 : CG)) {
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
                     sum[q][v] = red[(g * 4 + v) * 64 + lane];
 #pragma unroll
                     for (int w = 1; w < WAVES; ++w)
-                        sum[q][v] += red[((w * CG + g) * 4 + v) * 64 + lane];
+                        sum[q][v] = acc_add<E>(sum[q][v], red[((w * CG + g) * 4 + v) * 64 + lane]);
                 }
             if constexpr (SPLIT == 2) {
                 constexpr int GRP = GLU ? 1 : CG;  // groups with a counter of their own
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
 #pragma unroll
                             for (int q = 0; q < NG; ++q) {
                                 const f32x4 x = s0 + j == me ? own[q] : v[j][q];
-                                sum[q] = s0 + j == 0u ? x : sum[q] + x;
+                                sum[q] = s0 + j == 0u ? x : acc_add<E>(sum[q], x);
                             }
                 }
             }
@@ -278,7 +278,9 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm(P p)
                 for (int q = 0; q < NG; ++q)
                     sum[q] *= p.alpha;
             const int64_t row = 16 * slice + c16, col0 = n0 + (GLU ? 0 : 16 * wave) + 4 * h;
-            if ((int64_t)c16 < M)
+            if constexpr (EPI == EPI_OWN)
+                p.finish_quad(lane, row, col0, (int64_t)c16 < M, acc_value<E>(sum[0]));
+            else if ((int64_t)c16 < M)
                 for_act_kind(p.e.kind, [&](auto kind) __attribute__((always_inline)) {
                     constexpr int KIND = decltype(kind)::value;
 #pragma unroll

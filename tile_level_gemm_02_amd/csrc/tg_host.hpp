@@ -378,7 +378,7 @@ tg_status launch_nt(const P& a, int splits, hipStream_t s, int64_t grid_override
         return TG_ERR_NOT_SUPPORTED;
     constexpr int RB = NtStaging<E>::RB;
     constexpr int WM = NtWaves<E, BM, BN>::WM, WN = EPI == EPI_GLU && BN == 64 ? 1 : NtWaves<E, BM, BN>::WN;
-    if constexpr (!std::is_same<P, TileArgs>::value && ElemInfo<E>::bytes == 2 && BM == 256 && BN == 256) {
+    if constexpr (!std::is_same<P, TileArgs>::value && (ElemInfo<E>::bytes == 2 || E == E_I8) && BM == 256 && BN == 256) {
         // (five ring slots, four with both operands as k rows, whose moving
         // bases leave no registers for the addresses of five: 40 spills)
         constexpr int FNH = AL == A_MCONTIG ? 4 : 5;

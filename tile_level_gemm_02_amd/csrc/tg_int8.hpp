@@ -1,0 +1,198 @@
+// Products of int8 matrices with a scale for each token and each channel
+// (contract in include/tg_int8.h): their arguments, epilogue and plans.
+//
+//   Y = act(sx[m] sw[n] (x.W^T) + bias) + residual
+//
+// The sums are int32 and exact (K is held below 2^17); they are rounded to
+// fp32 once, then scaled.  The kernels are those of the other products: int8
+// rows have the same bytes per K step as 16-bit ones with twice the k, so the
+// copies, the ring and the fragments stay as they are and only the matrix
+// instruction (16x16x64, 32x32x32) and the accumulators' type differ.
+#pragma once
+
+#include "tg_fused.hpp"
+#include "tg_int8.h"
+
+namespace tg {
+
+struct I8Epi : EpiArgs {
+    const float* sx;  // [M]
+    const float* sw;  // [N]
+};
+
+template <int O>
+struct I8Args : TileArgs {
+    I8Epi e;
+
+    template <int RBK, int WR, int WC, int PBY, class Get>
+    __device__ __forceinline__ void finish(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, Get get) const
+    {
+        if constexpr (O != O_F32) {
+            // without a residual everything happens in the accumulator's layout,
+            // and rows go through LDS as 16 bits
+            if (e.R == nullptr) {
+                constexpr int G = 64 / RBK, NQ = WC / (4 * G), NB = WR / RBK;
+                float sx[NB], sw[4 * NQ], bias[4 * NQ];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int64_t row = row0 + i * RBK + lane % RBK;
+                    sx[i] = row < M ? e.sx[row] : 0.0f;
+                }
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int64_t col = col0 + q * 4 * G + 4 * (lane / RBK) + x;
+                        sw[4 * q + x] = col < N ? e.sw[col] : 0.0f;
+                        bias[4 * q + x] = e.bias != nullptr && col < N ? e.bias[col] : 0.0f;
+                    }
+                for_act_kind(e.kind, [&](auto kind) __attribute__((always_inline)) {
+                    store_rows16<O, RBK, WR, WC>(ep, lane, row0, col0, M, N, C, ldc, 0, true,
+                                                 [&](int i, int q) __attribute__((always_inline)) {
+                        f32x4 v = get(i, q);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            v[x] = act_value<decltype(kind)::value>(v[x] * (sx[i] * sw[4 * q + x]) + bias[4 * q + x], e);
+                        return v;
+                    });
+                });
+                return;
+            }
+        }
+        constexpr int VC = Piece<O>::N;
+        const int64_t col = col0 + lane % (WC / VC) * VC, left = N - col;
+        const int n = left >= VC ? VC : left > 0 ? (int)left : 0;
+        float sw[VC], bias[VC];
+#pragma unroll
+        for (int x = 0; x < VC; ++x) {
+            sw[x] = x < n ? e.sw[col + x] : 0.0f;
+            bias[x] = e.bias != nullptr && x < n ? e.bias[col + x] : 0.0f;
+        }
+        struct Row {
+            u32x4 r;
+            float sx;
+        };
+        for_act_kind(e.kind, [&](auto kind) __attribute__((always_inline)) {
+            staged_rows<VC, Row, RBK, WR, WC, PBY>(
+                ep, lane, row0, get,
+                [&](Row& s, int64_t row) __attribute__((always_inline)) {
+                    s.r = u32x4{0u, 0u, 0u, 0u};
+                    s.sx = 0.0f;
+                    if (row < M) {
+                        s.sx = e.sx[row];
+                        if (e.R != nullptr && n > 0)
+                            s.r = load_piece<O>(e.R, row * e.ldr + col, n, n == VC);
+                    }
+                },
+                [&](const Row& s, int64_t row, float* z) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int x = 0; x < VC; ++x)
+                        z[x] = act_value<decltype(kind)::value>(z[x] * (s.sx * sw[x]) + bias[x], e);
+                    if (e.R != nullptr)
+#pragma unroll
+                        for (int x = 0; x < VC; ++x)
+                            z[x] += piece_value<O>(s.r, x);
+                    if (row < M && n > 0)
+                        store_piece<O>(C, row * ldc + col, pack_piece<O>(z), n, n == VC);
+                });
+        });
+    }
+};
+
+template <int O>
+struct I8SkinnyArgs : SkinnyArgs {
+    I8Epi e;
+
+    __device__ __forceinline__ void finish_quad(uint32_t, int64_t row, int64_t col, bool in, f32x4 a) const
+    {
+        if (!in)
+            return;
+        const float sx = e.sx[row];
+        for_act_kind(e.kind, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (col + x < N) {
+                    const float z = a[x] * (sx * e.sw[col + x]) + (e.bias != nullptr ? e.bias[col + x] : 0.0f);
+                    float y = act_value<decltype(kind)::value>(z, e);
+                    if (e.R != nullptr)
+                        y += load_value<O>(e.R, row * e.ldr + col + x);
+                    store_value<O>(C, row * ldc + col + x, y);
+                }
+        });
+    }
+};
+
+// Rows up to which a call takes the skinny kernel
+constexpr int64_t kI8SkinnyRows = 32;
+
+template <int O, int AI, int SPLIT, int CG>
+void launch_i8_skinny(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipStream_t s)
+{
+    typedef SkinnyCfg G;
+    hipLaunchKernelGGL((skinny_gemm<E_I8, O, G::WAVES, AI, G::RING, SPLIT, CG, EPI_OWN, I8SkinnyArgs<O>>),
+                       dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * G::WAVES), 0, s, a);
+}
+
+template <int O, int SPLIT>
+void launch_i8_rows(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipStream_t s)
+{
+    if (a.M <= 8)
+        launch_i8_skinny<O, 1, SPLIT, 1>(a, blocks, split, s);
+    else if (fused_cg(a.M, a.N) == 1)
+        launch_i8_skinny<O, 2, SPLIT, 1>(a, blocks, split, s);
+    else
+        launch_i8_skinny<O, 2, SPLIT, 2>(a, blocks, split, s);
+}
+
+inline int64_t i8_ws_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || K % 16 != 0 || !dims_fit(M, N, K))
+        return 0;
+    if (M <= kI8SkinnyRows) {
+        const int64_t blocks = fused_skinny_blocks(M, N);
+        return fused_skinny_ws_bytes(M, N, blocks, fused_split<E_I8>(blocks, K));
+    }
+    return plan_nt<E_I8, B_KCONTIG>(M, N, K, true).ws_bytes;
+}
+
+template <int O>
+tg_status i8_linear(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_bytes, hipStream_t s)
+{
+    if (t.M <= kI8SkinnyRows && t.K > 0 && skinny_offsets_fit(t.K, t.lda, t.ldb, SkinnyCfg::RING, fused_cg(t.M, t.N))) {
+        I8SkinnyArgs<O> a{};
+        a.M = t.M;
+        a.N = t.N;
+        a.K = t.K;
+        a.A = t.A;
+        a.lda = t.lda;
+        a.B = t.B;
+        a.ldb = t.ldb;
+        a.C = t.C;
+        a.ldc = t.ldc;
+        a.e = e;
+        const int64_t blocks = fused_skinny_blocks(a.M, a.N);
+        if (blocks > 0x7FFFFFFF)
+            return TG_ERR_NOT_SUPPORTED;
+        const int split = fused_split<E_I8>(blocks, a.K);
+        const int64_t need = fused_skinny_ws_bytes(a.M, a.N, blocks, split);
+        if (ws != nullptr && need > 0 && need <= ws_bytes) {
+            a.counters = (uint32_t*)ws;
+            a.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+            launch_i8_rows<O, 2>(a, blocks, split, s);
+        } else {
+            launch_i8_rows<O, 0>(a, blocks, 1, s);
+        }
+        return launched();
+    }
+    I8Args<O> a{};
+    static_cast<TileArgs&>(a) = t;
+    a.e = e;
+    if (!nt_eligible<E_I8>(a))
+        return TG_ERR_NOT_SUPPORTED;
+    NtPlan plan = plan_nt<E_I8, B_KCONTIG>(a.M, a.N, a.K, ws != nullptr);
+    if (plan.ws_bytes > ws_bytes)
+        plan = plan_nt<E_I8, B_KCONTIG>(a.M, a.N, a.K, false);
+    return launch_nt_plan<E_I8, O, B_KCONTIG, EPI_OWN, A_KCONTIG>(a, plan, ws, s);
+}
+
+}  // namespace tg

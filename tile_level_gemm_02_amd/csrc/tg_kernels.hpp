@@ -443,6 +443,14 @@ template <> struct Mfma16<E_FP8> {
     }
 };
 
+// 16 int8 values per lane, k 64 together
+template <> struct Mfma16<E_I8> {
+    __device__ __forceinline__ static f32x4 run(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return bit_cast<f32x4>(__builtin_amdgcn_mfma_i32_16x16x64_i8(bit_cast<i32x4>(a), bit_cast<i32x4>(b), bit_cast<i32x4>(c), 0, 0, 0));
+    }
+};
+
 // Zero an M x N fp32 matrix with leading dimension ldc (the split skinny
 // GEMM adds its partial tiles into it); rows start 16-byte aligned.  Grid:
 // ceil(N / 1024) x M workgroups, 4 columns per lane.  A template only so

@@ -1,0 +1,732 @@
+// The vocabulary loss and its gradient (contracts in include/tg_train.h): the
+// epilogues of their products and the small kernels between them, one template
+// per input type, instantiated in that type's translation units.
+//
+//   t = scale x.W^T,  lse = log sum_v e^t,  loss = lse - t[target] + z lse^2
+//   dt = g (e^(t - lse) (1 + 2 z lse) - onehot),  dX = scale dt.W,  dW = scale dt^T.x
+//
+// The logits are never stored.  Forward: each wave of the product x.W^T holds
+// 64 columns of its rows and leaves two numbers per row, the largest t and the
+// sum of e^(t - largest) (xent_join adds them up over the vocabulary), and the
+// wave that holds a row's target leaves its t.  Gradient: a piece of the
+// vocabulary at a time, the same product again with dt as its epilogue,
+// rounded to 16 bits, then the two products that take dt as their operand.
+// All of them are bound by the matrix products: 2 M V D operations forward
+// and 6 for the gradient.
+//
+// Exponentials are base 2: with c = scale log2(e), e^(t - lse) is
+// exp2(acc c - lse log2(e)), one multiply-add and one instruction per value.
+#pragma once
+
+#include "tg_fused.hpp"
+#include "tg_train.h"
+
+namespace tg {
+
+constexpr int kXentCols = 64;  // columns of a wave's tile, in every tile the forward product takes
+
+// A row of the gradient's epilogue: exp2(acc c - lse2) a - (column == target ? b : 0)
+struct XentRow {
+    float lse2, a, b;
+    int32_t target;
+};
+
+// ------------------------------------------------------- forward epilogue
+struct XentOut {
+    float c, scale;
+    const int64_t* target;
+    f32x2_t* part;   // [slot][M]: largest t (base 2) and sum of 2^(t - largest) over the slot's columns
+    float* picked;   // [M]: t of the target
+};
+
+// One value per lane reduced over the lanes that hold the same row (RBK apart)
+template <int RBK, class F>
+__device__ __forceinline__ float over_row_lanes(float v, F f)
+{
+#pragma unroll
+    for (int d = RBK; d < 64; d *= 2)
+        v = f(v, __shfl_xor(v, d, 64));
+    return v;
+}
+
+__device__ __forceinline__ float max2(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+
+// reference of a sum of exponentials: 0 where there is none (all -infinity, or NaN)
+__device__ __forceinline__ float reference_of(float top) { return top == -INFINITY ? 0.0f : top; }
+
+struct XentFwdArgs : TileArgs {
+    XentOut x;
+
+    template <int RBK, int WR, int WC, int PBY, class Get>
+    __device__ __forceinline__ void finish(uint8_t*, uint32_t lane, int64_t row0, int64_t col0, Get get) const
+    {
+        constexpr int G = 64 / RBK, NQ = WC / (4 * G);
+        static_assert(WC == kXentCols, "a slot per wave");
+        if (col0 >= N)
+            return;
+        const int64_t slot = col0 / kXentCols;
+        const int left = N - col0 < WC ? (int)(N - col0) : WC;
+        const int lg = (int)(lane / RBK);
+        auto rows = [&](auto whole) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < WR / RBK; ++i) {
+                const int64_t row = row0 + i * RBK + lane % RBK;
+                float v[NQ * 4], top = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const f32x4 a = get(i, q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[4 * q + e] = a[e] * x.c;
+                        if (!decltype(whole)::value && q * 4 * G + 4 * lg + e >= left)
+                            v[4 * q + e] = -INFINITY;
+                        top = max2(top, v[4 * q + e]);
+                    }
+                }
+                top = over_row_lanes<RBK>(top, max2);
+                const float ref = reference_of(top);
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NQ * 4; ++k)
+                    sum += __builtin_amdgcn_exp2f(v[k] - ref);
+                sum = over_row_lanes<RBK>(sum, add2);
+                if (row < M) {
+                    if (lg == 0)
+                        x.part[slot * M + row] = f32x2_t{top, sum};
+                    const int64_t at = x.target[row] - col0;
+                    if (at >= 0 && at < left && (int)(at / 4) % G == lg) {
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            const f32x4 a = get(i, q);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if ((int)at == q * 4 * G + 4 * lg + e)
+                                    x.picked[row] = a[e] * x.scale;
+                        }
+                    }
+                }
+            }
+        };
+        if (left == WC)
+            rows(std::true_type{});
+        else
+            rows(std::false_type{});
+    }
+};
+
+// few rows: the skinny kernel, whose waves each hold 16 columns
+struct XentSkinnyArgs : SkinnyArgs {
+    XentOut x;
+
+    __device__ __forceinline__ void finish_quad(uint32_t lane, int64_t row, int64_t col, bool in, f32x4 a) const
+    {
+        const int left = N - col < 4 ? (int)(N - col) : 4;  // (<= 0 past the last column)
+        float v[4], top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = e < left ? a[e] * x.c : -INFINITY;
+            top = max2(top, v[e]);
+        }
+        top = over_row_lanes<16>(top, max2);
+        const float ref = reference_of(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum += __builtin_amdgcn_exp2f(v[e] - ref);
+        sum = over_row_lanes<16>(sum, add2);
+        const int64_t col16 = col & ~(int64_t)15;
+        if (!in || col16 >= N)
+            return;
+        if (lane < 16u)
+            x.part[col16 / 16 * M + row] = f32x2_t{top, sum};
+        const int64_t at = x.target[row] - col;
+        if (at >= 0 && at < left)
+            x.picked[row] = (at == 0 ? a[0] : at == 1 ? a[1] : at == 2 ? a[2] : a[3]) * x.scale;
+    }
+};
+
+// ---------------------------------------------------------- joining slots
+struct XentJoinArgs {
+    int64_t M, V, slots;
+    const f32x2_t* part;
+    const float* picked;
+    const int64_t* target;
+    int64_t ignore;
+    float z;
+    float *loss, *lse, *total;
+    uint32_t* counter;
+    double* sums;  // [workgroups][2]: losses and counted rows
+};
+
+__device__ __forceinline__ void join_pair(float& top, float& sum, float t, float s)
+{
+    const float m = max2(top, t), r = reference_of(m);
+    sum = sum * __builtin_amdgcn_exp2f(top - r) + s * __builtin_amdgcn_exp2f(t - r);
+    top = m;
+}
+
+// The slots of R rows per workgroup, 256 / R lanes to a row, several loads
+// ahead of their arithmetic.  Each lane's slots, and then the lanes, are added
+// in a fixed order.
+template <int R>
+__global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
+{
+    constexpr int T = 256 / R, B = 8;
+    __shared__ float red[2][T][R];
+    __shared__ double own[2][R];
+    __shared__ bool last;
+    const uint32_t tid = threadIdx.x, r = tid % R, part = tid / R;
+    const int64_t row = (int64_t)blockIdx.x * R + r;
+    float top = -INFINITY, sum = 0.0f;
+    if (row < p.M) {
+        for (int64_t s0 = part; s0 < p.slots; s0 += (int64_t)T * B) {
+            f32x2_t v[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int64_t s = s0 + (int64_t)b * T;
+                v[b] = f32x2_t{-INFINITY, 0.0f};
+                if (s < p.slots)
+                    v[b] = p.part[s * p.M + row];
+            }
+            float m = v[0][0];
+#pragma unroll
+            for (int b = 1; b < B; ++b)
+                m = max2(m, v[b][0]);
+            const float ref = reference_of(m);
+            float s = 0.0f;
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                s += v[b][1] * __builtin_amdgcn_exp2f(v[b][0] - ref);
+            join_pair(top, sum, m, s);
+        }
+    }
+    red[0][part][r] = top;
+    red[1][part][r] = sum;
+    __syncthreads();
+    if constexpr (T > 64) {  // (one row: 256 lanes' pairs become 64)
+        if (tid < 64u) {
+#pragma unroll
+            for (int k = 1; k < T / 64; ++k)
+                join_pair(top, sum, red[0][part + 64 * k][r], red[1][part + 64 * k][r]);
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1)
+                join_pair(top, sum, __shfl_xor(top, d, 64), __shfl_xor(sum, d, 64));
+        }
+    } else if (tid < (uint32_t)R) {
+        for (int k = 1; k < T; ++k)
+            join_pair(top, sum, red[0][k][r], red[1][k][r]);
+    }
+    if (tid < (uint32_t)R) {
+        double counted = 0.0, mine = 0.0;
+        if (row < p.M) {
+            const float lse = top * 0.693147180559945309f + logf(sum);
+            const int64_t t = p.target[row];
+            const bool counts = t != p.ignore;
+            float loss = 0.0f;
+            if (counts)
+                loss = t < 0 || t >= p.V ? NAN : lse - p.picked[row] + p.z * lse * lse;
+            if (p.lse != nullptr)
+                p.lse[row] = lse;
+            if (p.loss != nullptr)
+                p.loss[row] = loss;
+            counted = counts ? 1.0 : 0.0;
+            mine = (double)loss;
+        }
+        own[0][r] = mine;
+        own[1][r] = counted;
+    }
+    if (p.total == nullptr)
+        return;
+    // this workgroup's sums into its slot; the last to arrive adds all slots in order
+    __syncthreads();
+    if (tid == 0u) {
+        double a = 0.0, b = 0.0;
+        for (int k = 0; k < R; ++k) {
+            a += own[0][k];
+            b += own[1][k];
+        }
+        __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x, a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1u;
+    }
+    __syncthreads();
+    if (!last)
+        return;
+    __shared__ double all[2][256];
+    double a = 0.0, b = 0.0;
+    for (uint32_t k = tid; k < gridDim.x; k += 256u) {
+        a += __hip_atomic_load(p.sums + 2 * (size_t)k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        b += __hip_atomic_load(p.sums + 2 * (size_t)k + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    all[0][tid] = a;
+    all[1][tid] = b;
+    __syncthreads();
+    if (tid == 0u) {
+        for (int k = 1; k < 256; ++k) {
+            a += all[0][k];
+            b += all[1][k];
+        }
+        __hip_atomic_exchange(p.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        p.total[0] = (float)a;
+        p.total[1] = (float)b;
+    }
+}
+
+// ------------------------------------------------------ gradient epilogues
+// dt of a piece of the vocabulary, rounded to 16 bits; columns from N up to
+// the next multiple of 8 are written as zeros, since the product dt.W reads
+// whole 16-byte chunks of dt's rows.
+template <int O>
+struct XentGradArgs : TileArgs {
+    const XentRow* rows;
+    float c;
+    int64_t v0;  // first column of the piece
+
+    template <int RBK, int WR, int WC, int PBY, class Get>
+    __device__ __forceinline__ void finish(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, Get get) const
+    {
+        constexpr int G = 64 / RBK, NB = WR / RBK;
+        const int64_t padded = (N + 7) / 8 * 8;
+        if (col0 >= padded)
+            return;
+        const int lg4 = 4 * (int)(lane / RBK);
+        const int left = N - col0 < WC ? (int)(N - col0) : WC;
+        XentRow r[NB];
+        int at[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t row = row0 + i * RBK + lane % RBK;
+            r[i] = XentRow{0.0f, 0.0f, 0.0f, -1};
+            if (row < M)
+                r[i] = rows[row];
+            const int64_t k = (int64_t)r[i].target - v0 - col0;
+            at[i] = k >= 0 && k < WC ? (int)k : -1;
+        }
+        store_rows16<O, RBK, WR, WC>(ep, lane, row0, col0, M, padded, C, ldc, 0, true,
+                                     [&](int i, int q) __attribute__((always_inline)) {
+            const f32x4 v = get(i, q);
+            f32x4 d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = q * 4 * G + lg4 + e;
+                d[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], c, -r[i].lse2)) * r[i].a;
+                d[e] = col == at[i] ? d[e] - r[i].b : d[e];
+                // (an ignored row is zero whatever its logits; NaN is not equal to 0)
+                d[e] = (r[i].a == 0.0f && r[i].b == 0.0f) || col >= left ? 0.0f : d[e];
+            }
+            return d;
+        });
+    }
+};
+
+// The products that take dt: C = alpha (acc + R), alpha in device memory, R
+// the fp32 sums over the pieces before (or null).  O_F32 with alpha null
+// keeps such sums.
+template <int O>
+struct XentProdArgs : TileArgs {
+    const float* factor;  // null: 1
+    const float* R;
+    int64_t ldr;
+
+    template <int RBK, int WR, int WC, int PBY, class Get>
+    __device__ __forceinline__ void finish(uint8_t* ep, uint32_t lane, int64_t row0, int64_t col0, Get get) const
+    {
+        const float f = factor != nullptr ? *factor : 1.0f;
+        if constexpr (O != O_F32) {
+            if (R == nullptr) {
+                store_rows16<O, RBK, WR, WC>(ep, lane, row0, col0, M, N, C, ldc, 0, true,
+                                             [&](int i, int q) __attribute__((always_inline)) { return get(i, q) * f; });
+                return;
+            }
+        }
+        constexpr int VC = Piece<O>::N;
+        const int64_t col = col0 + lane % (WC / VC) * VC, left = N - col;
+        const int n = left >= VC ? VC : left > 0 ? (int)left : 0;
+        struct Sums {
+            u32x4 q[VC / 4];
+        };
+        staged_rows<VC, Sums, RBK, WR, WC, PBY>(
+            ep, lane, row0, get,
+            [&](Sums& s, int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+                for (int h = 0; h < VC / 4; ++h) {
+                    const int m = n - 4 * h < 4 ? n - 4 * h : 4;
+                    s.q[h] = u32x4{0u, 0u, 0u, 0u};
+                    if (R != nullptr && row < M && m > 0)
+                        s.q[h] = load_piece<O_F32>(R, row * ldr + col + 4 * h, m, m == 4);
+                }
+            },
+            [&](const Sums& s, int64_t row, float* z) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < VC; ++e)
+                    z[e] = (z[e] + piece_value<O_F32>(s.q[e / 4], e % 4)) * f;
+                if (row < M && n > 0)
+                    store_piece<O>(C, row * ldc + col, pack_piece<O>(z), n, n == VC);
+            });
+    }
+};
+
+// --------------------------------------------------------- gradient's rows
+struct XentRowsArgs {
+    int64_t M, V;
+    const int64_t* target;
+    int64_t ignore;
+    float z, scale, grad_scale, lift;  // lift: 2^12 for fp16, 1 for bf16
+    const float *lse, *dloss, *total;
+    XentRow* rows;
+    float* factor;
+};
+
+// One workgroup: the largest factor of a row that counts, as a power of two at
+// or above it, and each row's numbers relative to it.  What it divides out (and
+// `lift`) returns in the products' factor.
+template <int = 0>
+__global__ __launch_bounds__(1024) void xent_rows(XentRowsArgs p)
+{
+    __shared__ float red[16];
+    const uint32_t tid = threadIdx.x;
+    float most = 1.0f;
+    if (p.dloss != nullptr || p.z != 0.0f) {
+        most = 0.0f;
+        for (int64_t i = tid; i < p.M; i += 1024)
+            if (p.target[i] != p.ignore) {
+                const float b = p.dloss != nullptr ? __builtin_fabsf(p.dloss[i]) : 1.0f;
+                most = max2(most, max2(b, b * __builtin_fabsf(1.0f + 2.0f * p.z * p.lse[i])));
+            }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            most = max2(most, __shfl_xor(most, d, 64));
+        if ((tid & 63u) == 0u)
+            red[tid >> 6] = most;
+        __syncthreads();
+        for (int k = 0; k < 16; ++k)
+            most = max2(most, red[k]);
+    }
+    // 2^e >= most, within fp32's normal numbers (infinity, and none at all: 1)
+    int e = 0;
+    if (most > 0.0f && most < INFINITY) {
+        (void)frexpf(most, &e);
+        e = e < -100 ? -100 : e;
+    }
+    const float down = ldexpf(1.0f, -e) * p.lift;  // (e <= 128, lift <= 2^12: a normal number or a subnormal 2^-128)
+    for (int64_t i = tid; i < p.M; i += 1024) {
+        const int64_t t = p.target[i];
+        XentRow r{0.0f, 0.0f, 0.0f, -1};
+        if (t != p.ignore) {
+            const bool known = t >= 0 && t < p.V;
+            const float lse = p.lse[i];
+            r.lse2 = lse * 1.44269504088896341f;
+            r.b = known ? (p.dloss != nullptr ? p.dloss[i] * down : down) : NAN;
+            r.a = r.b * (1.0f + 2.0f * p.z * lse);
+            r.target = known ? (int32_t)t : -1;
+        }
+        p.rows[i] = r;
+    }
+    if (tid == 0u) {
+        const float count = p.total != nullptr ? max2(p.total[1], 1.0f) : 1.0f;
+        *p.factor = (float)((double)p.scale * (double)p.grad_scale * ldexp(1.0, e) / ((double)p.lift * (double)count));
+    }
+}
+
+// --------------------------------------------------------------- host side
+inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// forward: the skinny kernel's rows, as for tg_linear
+template <int E>
+bool xent_skinny(int64_t M, int64_t D, int64_t ldx, int64_t ldw, int64_t V)
+{
+    return M <= kFusedSkinnyRows<E> && D > 0 && skinny_offsets_fit(D, ldx, ldw, SkinnyCfg::RING, fused_cg(M, V));
+}
+
+struct XentFwd {
+    int64_t slots, part, picked, sums, bytes;  // offsets and bytes in the workspace
+    int join_rows;
+};
+
+// rows per workgroup of xent_join: one where there are few, which then take 256 lanes each
+inline int xent_join_rows(int64_t M) { return M <= 64 ? 1 : 16; }
+
+// (slots of 16 columns for few rows, whichever kernel then takes them)
+inline XentFwd xent_fwd_layout(int64_t M, int64_t V, int64_t few)
+{
+    XentFwd f{};
+    const int64_t cols = M <= few ? 16 : kXentCols;
+    f.slots = (V + cols - 1) / cols;
+    f.join_rows = xent_join_rows(M);
+    f.part = kSplitCounterBytes;
+    f.picked = up(f.part + f.slots * M * 8, 256);
+    f.sums = up(f.picked + M * 4, 256);
+    f.bytes = up(f.sums + (M + f.join_rows - 1) / f.join_rows * 16, 256);
+    return f;
+}
+
+struct XentCall {
+    int64_t M, V, D;
+    const void* x;
+    int64_t ldx;
+    const void* W;
+    int64_t ldw;
+    float scale;
+    const int64_t* target;
+    int64_t ignore;
+    float z;
+    // forward
+    float *loss, *lse_out, *total_out;
+    // gradient
+    const float *lse, *dloss, *total;
+    float grad_scale;
+    void* dX;
+    int64_t lddx;
+    void* dW;
+    int64_t lddw;
+    int dw_dtype;
+    void* ws;
+    int64_t ws_bytes;
+    hipStream_t s;
+};
+
+inline float xent_c(float scale) { return (float)((double)scale * 1.4426950408889634074); }
+
+template <int E, int AI, int CG>
+void launch_xent_skinny(const XentSkinnyArgs& a, int64_t blocks, hipStream_t s)
+{
+    typedef SkinnyCfg G;
+    hipLaunchKernelGGL((skinny_gemm<E, O_F32, G::WAVES, AI, G::RING, 0, CG, EPI_OWN, XentSkinnyArgs>), dim3((uint32_t)blocks),
+                       dim3(64 * G::WAVES), 0, s, a);
+}
+
+template <int E>
+tg_status xent_forward(const XentCall& q)
+{
+    const XentFwd f = xent_fwd_layout(q.M, q.V, kFusedSkinnyRows<E>);
+    uint8_t* const ws = (uint8_t*)q.ws;
+    XentOut o{xent_c(q.scale), q.scale, q.target, (f32x2_t*)(ws + f.part), (float*)(ws + f.picked)};
+    int64_t slots = f.slots;
+    if (q.M == 0) {
+        // (only the total, of no rows)
+    } else if (xent_skinny<E>(q.M, q.D, q.ldx, q.ldw, q.V)) {
+        XentSkinnyArgs a{};
+        a.M = q.M;
+        a.N = q.V;
+        a.K = q.D;
+        a.A = (const uint8_t*)q.x;
+        a.lda = q.ldx;
+        a.B = (const uint8_t*)q.W;
+        a.ldb = q.ldw;
+        a.x = o;
+        const int64_t blocks = fused_skinny_blocks(q.M, q.V);
+        if (blocks > 0x7FFFFFFF)
+            return TG_ERR_NOT_SUPPORTED;
+        if (q.M <= 8)
+            launch_xent_skinny<E, 1, 1>(a, blocks, q.s);
+        else if (fused_cg(q.M, q.V) == 1)
+            launch_xent_skinny<E, 2, 1>(a, blocks, q.s);
+        else
+            launch_xent_skinny<E, 2, 2>(a, blocks, q.s);
+    } else {
+        slots = (q.V + kXentCols - 1) / kXentCols;
+        XentFwdArgs a{};
+        set_product(a, q.M, q.V, q.D, q.x, q.ldx, q.W, q.ldw, nullptr, 0, 1.0f);
+        a.x = o;
+        a.group_m = 4;
+        a.splits = 1;
+        if (!nt_eligible<E>(a))
+            return TG_ERR_NOT_SUPPORTED;
+        // tiles whose waves hold 64 columns: no 64 x 64 ones
+        const NtPlan p = plan_nt<E, B_KCONTIG>(q.M, q.V, q.D, false);
+        tg_status st = TG_OK;
+        if (p.tile == 256 && p.tn == 128) {
+            st = launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(a, 1, q.s);
+        } else if (p.tile == 256 && p.tail == kTailNone) {
+            st = launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, q.s);
+        } else if (p.tile == 256) {
+            XentFwdArgs b = a;
+            const int64_t rest = n_tiles<256, 256>(a.M, a.N) - p.dp;
+            a.dp = (uint32_t)p.dp;
+            st = launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, q.s, p.dp);
+            b.sub256 = (uint32_t)p.dp + 1u;
+            if (st == TG_OK)
+                st = p.tail == kTailWide ? launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(b, 1, q.s, 2 * rest)
+                                         : launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(b, 1, q.s, 4 * rest);
+        } else if (n_tiles<128, 128>(a.M, a.N) <= 256) {
+            st = launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(a, 1, q.s);
+        } else {
+            st = launch_nt<E, O_F32, 128, 128, B_KCONTIG, 4, EPI_OWN, A_KCONTIG>(a, 1, q.s);
+        }
+        if (st != TG_OK)
+            return st;
+    }
+    XentJoinArgs j{};
+    j.M = q.M;
+    j.V = q.V;
+    j.slots = slots;
+    j.part = o.part;
+    j.picked = o.picked;
+    j.target = q.target;
+    j.ignore = q.ignore;
+    j.z = q.z;
+    j.loss = q.loss;
+    j.lse = q.lse_out;
+    j.total = q.total_out;
+    j.counter = (uint32_t*)ws;
+    j.sums = (double*)(ws + f.sums);
+    const int64_t grid = q.M == 0 ? 1 : (q.M + f.join_rows - 1) / f.join_rows;
+    if (f.join_rows == 1)
+        hipLaunchKernelGGL(xent_join<1>, dim3((uint32_t)grid), dim3(256), 0, q.s, j);
+    else
+        hipLaunchKernelGGL(xent_join<16>, dim3((uint32_t)grid), dim3(256), 0, q.s, j);
+    return launched();
+}
+
+// Columns of a piece: dt takes at most kXentPieceBytes, and a piece's rows of
+// W lie within one buffer descriptor (as nt_eligible_nrow asks).
+constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
+
+inline int64_t xent_most_piece(int64_t M, int64_t V, int64_t ldw)
+{
+    int64_t most = kXentPieceBytes / (2 * (M < 1 ? 1 : M)) / 256 * 256;
+    most = most < 256 ? 256 : most;
+    const int64_t fits = ((int64_t)kNumRecords - 1024) / (2 * (ldw < 1 ? 1 : ldw)) - 512;
+    if (most > 131072)
+        most = 131072;
+    if (most > fits / 256 * 256)
+        most = fits / 256 * 256;
+    if (most > up(V, 256))
+        most = up(V, 256);
+    return most;
+}
+
+// Pieces of equal size (multiples of 256, the last one the rest) of at most `most` columns
+inline int64_t xent_even(int64_t V, int64_t most)
+{
+    const int64_t pieces = (V + most - 1) / most;
+    return up((V + pieces - 1) / pieces, 256);
+}
+
+// partial tiles of any split plan: one round of 256 x 256 fp32
+constexpr int64_t kXentSplitBytes = (int64_t)64 << 20;
+
+struct XentBwd {
+    int64_t piece, pieces, ldz;
+    int64_t rows, factor, sums, dz, bytes;  // offsets and bytes in the workspace
+};
+
+inline XentBwd xent_bwd_layout(int64_t M, int64_t V, int64_t D, int64_t piece)
+{
+    XentBwd b{};
+    b.piece = piece;
+    b.pieces = (V + piece - 1) / piece;
+    b.ldz = piece;
+    b.rows = kSplitCounterBytes + kXentSplitBytes;
+    b.factor = up(b.rows + M * (int64_t)sizeof(XentRow), 256);
+    b.sums = b.factor + 256;
+    b.dz = up(b.sums + (b.pieces > 1 ? M * up(D, 4) * 4 : 0), 256);
+    b.bytes = b.dz + M * b.ldz * 2;
+    return b;
+}
+
+// The layout with the fewest pieces that `ws_bytes` hold; bytes 0 if none does
+inline XentBwd xent_bwd_plan(int64_t M, int64_t V, int64_t D, int64_t most, int64_t ws_bytes)
+{
+    int64_t last = 0;
+    for (int64_t k = (V + most - 1) / most; k <= (V + 255) / 256; ++k) {
+        const int64_t piece = up((V + k - 1) / k, 256);
+        if (piece == last || piece > most)
+            continue;
+        last = piece;
+        const XentBwd b = xent_bwd_layout(M, V, D, piece);
+        if (b.bytes <= ws_bytes)
+            return b;
+        if (piece == 256)
+            break;
+    }
+    return XentBwd{};
+}
+
+inline int64_t xent_bwd_bytes(int64_t M, int64_t V, int64_t D, int64_t ldw, int64_t piece)
+{
+    const int64_t most = xent_most_piece(M, V, ldw);
+    if (most < 256)
+        return -1;
+    piece = piece == 0 ? xent_even(V, most) : piece > most ? xent_even(V, most) : up(piece, 256);
+    return xent_bwd_layout(M, V, D, piece).bytes;
+}
+
+// dt of a piece
+template <int E>
+tg_status xent_dz(const TileArgs& t, const XentRow* rows, float c, int64_t v0, hipStream_t s)
+{
+    XentGradArgs<OutOf<E>::O> a{};
+    static_cast<TileArgs&>(a) = t;
+    a.rows = rows;
+    a.c = c;
+    a.v0 = v0;
+    if (!nt_eligible<E>(a))
+        return TG_ERR_NOT_SUPPORTED;
+    return launch_nt_plan<E, OutOf<E>::O, B_KCONTIG, EPI_OWN, A_KCONTIG>(a, plan_nt<E, B_KCONTIG>(a.M, a.N, a.K, false), nullptr, s);
+}
+
+// A product that takes dt (which may end inside a 16-byte chunk: the rest of
+// it is zeros, or feeds rows that are not stored)
+template <int E, int O, int AL>
+tg_status xent_product(const TileArgs& t, const float* factor, const float* R, int64_t ldr, void* ws, hipStream_t s)
+{
+    XentProdArgs<O> a{};
+    static_cast<TileArgs&>(a) = t;
+    a.factor = factor;
+    a.R = R;
+    a.ldr = ldr;
+    return launch_nt_plan<E, O, B_NCONTIG, EPI_OWN, AL>(a, plan_nt<E, B_NCONTIG>(a.M, a.N, a.K, true), ws, s);
+}
+
+// (defined in the translation units of their kernels)
+template <int E> tg_status xent_xgrad(const TileArgs& t, bool last, const float* factor, const float* R, int64_t ldr, void* ws, hipStream_t s);
+template <int E> tg_status xent_wgrad(const TileArgs& t, int dtype, const float* factor, void* ws, hipStream_t s);
+template <> tg_status xent_xgrad<E_F16>(const TileArgs&, bool, const float*, const float*, int64_t, void*, hipStream_t);
+template <> tg_status xent_xgrad<E_BF16>(const TileArgs&, bool, const float*, const float*, int64_t, void*, hipStream_t);
+template <> tg_status xent_wgrad<E_F16>(const TileArgs&, int, const float*, void*, hipStream_t);
+template <> tg_status xent_wgrad<E_BF16>(const TileArgs&, int, const float*, void*, hipStream_t);
+
+template <int E>
+tg_status xent_backward(const XentCall& q)
+{
+    const int64_t most = xent_most_piece(q.M, q.V, q.ldw);
+    if (most < 256)
+        return TG_ERR_NOT_SUPPORTED;
+    const XentBwd b = xent_bwd_plan(q.M, q.V, q.D, most, q.ws_bytes);
+    if (b.bytes == 0)
+        return TG_ERR_INVALID_VALUE;
+    uint8_t* const ws = (uint8_t*)q.ws;
+    XentRow* const rows = (XentRow*)(ws + b.rows);
+    float* const factor = (float*)(ws + b.factor);
+    float* const sums = (float*)(ws + b.sums);
+    const int64_t lds = up(q.D, 4);
+    XentRowsArgs r{q.M, q.V, q.target, q.ignore, q.z, q.scale, q.grad_scale, E == E_F16 ? 4096.0f : 1.0f, q.lse, q.dloss, q.total, rows, factor};
+    hipLaunchKernelGGL(xent_rows<>, dim3(1), dim3(1024), 0, q.s, r);
+    tg_status st = launched();
+    for (int64_t i = 0; i < b.pieces && st == TG_OK; ++i) {
+        const int64_t v0 = i * b.piece, n = q.V - v0 < b.piece ? q.V - v0 : b.piece;
+        const uint8_t* const Wp = (const uint8_t*)q.W + v0 * q.ldw * 2;
+        void* const dz = ws + b.dz;
+        if (q.M > 0) {
+            TileArgs t{};
+            set_product(t, q.M, n, q.D, q.x, q.ldx, Wp, q.ldw, dz, b.ldz, 1.0f);
+            st = xent_dz<E>(t, rows, xent_c(q.scale), v0, q.s);
+            if (st == TG_OK && q.dX != nullptr) {
+                const bool last = i == b.pieces - 1;
+                set_product(t, q.M, q.D, n, dz, b.ldz, Wp, q.ldw, last ? q.dX : sums, last ? q.lddx : lds, 1.0f);
+                st = xent_xgrad<E>(t, last, last ? factor : nullptr, i > 0 ? sums : nullptr, lds, q.ws, q.s);
+            }
+        }
+        if (st == TG_OK && q.dW != nullptr) {
+            TileArgs t{};
+            set_product(t, n, q.D, q.M, dz, b.ldz, q.x, q.ldx, (uint8_t*)q.dW + v0 * q.lddw * out_bytes(q.dw_dtype), q.lddw, 1.0f);
+            st = xent_wgrad<E>(t, q.dw_dtype, factor, q.ws, q.s);
+        }
+    }
+    return st;
+}
+
+}  // namespace tg
