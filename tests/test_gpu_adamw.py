@@ -1,0 +1,259 @@
+"""tg_adamw on the GPU against its 64-bit definition: every combination of
+types, 32- and 8-bit states, sizes and alignments, clipping by a norm, steps
+that are left out, and captured steps."""
+import itertools
+
+import pytest
+import torch
+
+from _train_ref import BLOCK, E4M3_MAX, E4M3_STEP, TINY, U, adamw, held, rounded, within
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32, F8 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+HYPER = dict(lr=1e-2, b1=0.9, b2=0.95, eps=1e-8, wd=0.1)
+
+
+@pytest.fixture(scope="module")
+def tg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import tile_level_gemm_02_amd as tg
+
+    return tg
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def view(t, shift):
+    """The same values `shift` elements past an aligned start, and values behind that have to stay."""
+    n = t.numel()
+    s = torch.zeros(n + shift + 8, device="cuda", dtype=torch.float32).to(t.dtype)
+    s.view(torch.uint8)[:] = 77
+    v = s[shift:shift + n]
+    v.copy_(t)
+    return s, v
+
+
+class Tensor:
+    """One tensor's buffers and its values before the step."""
+
+    def __init__(self, n, p, g, master, eight, seed, shift=0):
+        r = lambda std, k: torch.empty(n, device="cuda").normal_(0.0, std, generator=gen(seed + k))  # noqa: E731
+        self.n, self.shift, self.eight = n, shift, eight
+        w = r(0.5, 0)
+        self.s, self.t = {}, {}
+        self.add("p", w.to(p))
+        self.add("g", r(0.1, 1).to(g))
+        if master:
+            self.add("w", w)
+        m, root = r(0.03, 2), r(0.1, 3).abs()
+        if n > 2:
+            root[n // 2] = 0.0
+            m[n // 2] = 0.0
+        if eight:
+            blocks = -(-n // BLOCK)
+            for name, v in (("m", m), ("v", root)):
+                scale = torch.rand(blocks, device="cuda", generator=gen(seed + 4)) * 1e-3
+                q = (v / scale.repeat_interleave(BLOCK)[:n]).clamp(-448, 448).to(F8)
+                self.add(name, q)
+                self.t["s" + name] = scale
+        else:
+            self.add("m", m)
+            self.add("v", root * root)
+        self.before = {k: v.clone() for k, v in self.t.items()}
+
+    def add(self, name, t):
+        self.s[name], self.t[name] = view(t, self.shift)
+
+    def state(self, name, t):
+        v = t[name]
+        if not self.eight:
+            return v.double()
+        v = held(v, t["s" + name], self.n)
+        return v if name == "m" else v * v
+
+    def check(self, step, norm=None, max_norm=float("inf"), h=HYPER):
+        b, t = self.before, self.t
+        w0 = b.get("w", b["p"]).double()
+        w, m, v, up = adamw(w0, b["g"], self.state("m", b), self.state("v", b), step, h["lr"], h["b1"], h["b2"], h["eps"], h["wd"], norm, max_norm)
+        g = b["g"].double().abs()
+        m0, v0 = self.state("m", b).abs(), self.state("v", b)
+        # m and v: constants, products and one addition, 4 u of each part (8-bit states: 2 u more for what they stand for, squared)
+        dm, dv = 6 * U * (m0 + g) + 1e-45, 9 * U * (v0 + g * g) + 1e-45
+        # the update: m's error relative to it, v's at half weight, root, reciprocal, constants, products: 12 u
+        root = (v / (1 - h["b2"] ** step)).sqrt() + h["eps"]
+        size = h["lr"] / (1 - h["b1"] ** step) / root
+        dw = size * dm + up.abs() * (12 * U + 0.5 * dv / v.clamp(min=1e-60)) + 4 * U * w0.abs()
+        name = "w" if "w" in t else "p"
+        within(t[name], w, dw + rounded(w, t[name].dtype), name)
+        if "w" in t:
+            assert torch.equal(t["p"], t["w"].to(t["p"].dtype))
+        if not self.eight:
+            within(t["m"], m, dm, "m")
+            within(t["v"], v, dv, "v")
+        else:
+            for name, x, dx, lift in (("m", m, dm, False), ("v", v.sqrt(), 0.5 * dv / v.sqrt().clamp(min=1e-30) + 2 * U * v.sqrt(), True)):
+                self.check_eight(name, x, dx, lift)
+        assert torch.equal(t["g"], b["g"])
+        for k, s in self.s.items():
+            raw = s.view(torch.uint8)
+            item = s.element_size()
+            assert bool((raw[:self.shift * item] == 77).all()) and bool((raw[(self.shift + self.n) * item:] == 77).all()), f"{k}: wrote outside"
+
+    def check_eight(self, name, x, dx, lift):
+        q, scale = self.t[name].double(), self.t["s" + name].double()
+        pad = -self.n % BLOCK
+        block = lambda a: torch.nn.functional.pad(a, (0, pad)).view(-1, BLOCK)  # noqa: E731
+        top = block(x.abs()).amax(1)
+        within(self.t["s" + name], torch.where(top < TINY, 0.0, top / E4M3_MAX), 3 * U * top / E4M3_MAX + block(dx).amax(1) / E4M3_MAX, "scale of " + name)
+        unit = scale.repeat_interleave(BLOCK)[:self.n]
+        # half a step of e4m3 of the value, or of its smallest numbers; 4 u of the quotient, and the value's own error
+        near = (2.0 ** -4 * x.abs()).clamp(min=E4M3_STEP / 2 * unit) * (1 + 2.0 ** -10) + dx + 4 * U * x.abs()
+        if lift:
+            lifted = (x > 0) & (x < E4M3_STEP * unit)
+            near = torch.where(lifted, E4M3_STEP * unit, near)
+            assert bool((q[(x > 1e-38) & (unit > 0)] > 0).all()), "a root was rounded to zero"
+        assert bool(((q * unit - x).abs() <= near + 1e-45).all()), f"{name}: off by {float(((q * unit - x).abs() / (near + 1e-45)).max()):.3g} of its bound"
+
+
+def step_of(tg, tensors, step, **more):
+    L = lambda k: [t.t[k] for t in tensors]  # noqa: E731
+    eight, master = tensors[0].eight, any("w" in t.t for t in tensors)
+    h = HYPER
+    tg.tg_adamw(L("p"), L("g"), L("m"), L("v"), step, more.pop("lr", h["lr"]), betas=(h["b1"], h["b2"]), eps=h["eps"], weight_decay=h["wd"],
+                masters=L("w") if master else None, exp_avg_scales=L("sm") if eight else None, exp_avg_sq_scales=L("sv") if eight else None, **more)
+    torch.cuda.synchronize()
+
+
+SIZES = (1, 3, 8, 255, 256, 257, 4096, 4099, 10001, 300000)
+
+
+@pytest.mark.parametrize("p,g,master", [(p, g, m) for p, g, m in itertools.product((F32, BF, F16), (F32, BF, F16), (False, True))
+                                        if not (m and p == F32)])
+@pytest.mark.parametrize("eight", [False, True])
+def test_types(tg, p, g, master, eight):
+    for step, shift in ((1, 0), (1000, 3)):
+        print(p, g, master, eight, step, flush=True)
+        ts = [Tensor(n, p, g, master, eight, 10 * i, shift) for i, n in enumerate(SIZES)]
+        step_of(tg, ts, step)
+        for t in ts:
+            t.check(step)
+
+
+def test_mixed_types_and_many_tensors(tg):
+    ts = [Tensor(1 + 97 * i % 5000, (F32, BF, F16)[i % 3], (BF, F32)[i // 3 % 2], False, False, i, i % 5) for i in range(130)]
+    ts.insert(60, Tensor(0, F32, F32, False, False, 1))
+    step_of(tg, ts, 7)
+    for t in ts:
+        if t.n:
+            t.check(7)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_clipped_and_left_out(tg, eight):
+    for norm, most in ((4.0, 1.0), (0.5, 1.0), (4.0, float("inf")), (3.0, 0.0)):
+        t = Tensor(5000, BF, BF, True, eight, 3)
+        step_of(tg, [t], 5, norm=torch.tensor([norm], device="cuda"), max_norm=most)
+        t.check(5, norm, most)
+    for norm in (float("nan"), float("inf")):
+        t = Tensor(5000, BF, BF, True, eight, 3)
+        step_of(tg, [t], 5, norm=torch.tensor([norm], device="cuda"), max_norm=1.0)
+        for k, v in t.before.items():
+            assert torch.equal(v.view(torch.uint8), t.t[k].view(torch.uint8)), k
+
+
+def test_after_the_norm_of_the_gradients(tg):
+    """tg_clip_grads that clips nothing, and a step that clips by the norm it found."""
+    ts = [Tensor(n, BF, BF, False, False, n) for n in (100, 7000)]
+    norm = torch.empty(1, device="cuda")
+    tg.tg_clip_grads([t.t["g"] for t in ts], float("inf"), norm=norm, workspace=tg.tg_ops_workspace())
+    step_of(tg, ts, 2, norm=norm, max_norm=1.0)
+    want = float(sum(t.before["g"].double().square().sum() for t in ts)) ** 0.5
+    assert abs(float(norm) / want - 1) < 2.0 ** -23
+    for t in ts:
+        t.check(2, want, 1.0)
+
+
+def test_gradients_of_zero_and_empty_blocks(tg):
+    for eight in (False, True):
+        t = Tensor(1000, F32, F32, False, eight, 1)
+        for k in ("g", "m", "v"):
+            t.t[k].view(torch.uint8).zero_()
+        for k in ("sm", "sv"):
+            if k in t.t:
+                t.t[k].zero_()
+        t.before = {k: v.clone() for k, v in t.t.items()}
+        step_of(tg, [t], 3)
+        t.check(3)
+        assert not bool(t.t["m"].view(torch.uint8).any()) and not bool(t.t["v"].view(torch.uint8).any())
+    # a block whose largest value is below 2^-100 is held as zeros, and its neighbour as it is
+    t = Tensor(512, F32, F32, False, True, 1)
+    for k in ("m", "v"):
+        t.t[k].view(torch.uint8).zero_()
+    t.t["g"].fill_(1e-20)  # v' = 0.05 e-40, m' = 1e-21: m above 2^-100 = 7.9e-31, so is the root 2.2e-21
+    t.t["g"][256:] = 1e-35
+    t.before = {k: v.clone() for k, v in t.t.items()}
+    step_of(tg, [t], 3)
+    assert float(t.t["sm"][1]) == 0.0 and float(t.t["sm"][0]) > 0 and not bool(t.t["m"][256:].view(torch.uint8).any())
+
+
+def test_a_gradient_that_is_not_finite(tg):
+    """Without a norm to tell, NaN stays where it is: in its element, and with 8-bit states in no other's value."""
+    for eight in (False, True):
+        t = Tensor(1000, F32, F32, False, eight, 1)
+        t.t["g"][300] = float("nan")
+        step_of(tg, [t], 3)
+        for k in ("p", "m", "v"):
+            bad = t.t[k].float().isnan()
+            assert int(bad.sum()) == 1 and bool(bad[300]), (k, eight)
+
+
+def test_steps_in_device_memory_and_captured(tg):
+    """A captured step whose counter and rate move on in device memory equals eager steps, on three replays."""
+    for eight in (False, True):
+        a, b = (Tensor(9000, BF, BF, True, eight, 5) for _ in range(2))
+        step, lr = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.full((1,), 1e-2, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step.add_(1)
+            step_of_captured(tg, b, step, lr)
+        for k in range(1, 4):
+            for t in (a, b):
+                t.t["g"].copy_(torch.empty(9000, device="cuda").normal_(0.0, 0.1, generator=gen(70 + k)))
+            lr.fill_(1e-2 / k)
+            step_of(tg, [a], k, lr=float(lr))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert int(step) == k
+            for name in a.t:
+                assert torch.equal(a.t[name].view(torch.uint8), b.t[name].view(torch.uint8)), (k, name)
+
+
+def step_of_captured(tg, t, step, lr):
+    h, s = HYPER, t.t
+    tg.tg_adamw([s["p"]], [s["g"]], [s["m"]], [s["v"]], step, lr, betas=(h["b1"], h["b2"]), eps=h["eps"], weight_decay=h["wd"],
+                masters=[s["w"]], exp_avg_scales=[s["sm"]] if t.eight else None, exp_avg_sq_scales=[s["sv"]] if t.eight else None)
+
+
+def test_a_tensor_past_32_bit_offsets(tg):
+    n = (1 << 31) + 5000
+    for eight in (False, True):
+        p, g = torch.empty(n, device="cuda", dtype=BF).fill_(0.5), torch.empty(n, device="cuda", dtype=BF).fill_(0.25)
+        st = F8 if eight else F32
+        m, v = torch.zeros(n, device="cuda", dtype=torch.uint8 if eight else F32), torch.zeros(n, device="cuda", dtype=torch.uint8 if eight else F32)
+        m, v = m.view(st), v.view(st)
+        scales = [torch.zeros(-(-n // BLOCK), device="cuda") for _ in range(2)] if eight else [None, None]
+        g[-1] = -1.0
+        tg.tg_adamw([p], [g], [m], [v], 1, 1e-2, betas=(0.9, 0.95), weight_decay=0.0, exp_avg_scales=[scales[0]] if eight else None,
+                    exp_avg_sq_scales=[scales[1]] if eight else None)
+        # the first step moves each weight by lr against its gradient's sign
+        assert abs(float(p[0]) - 0.49) < 2.0 ** -9 and abs(float(p[-1]) - 0.51) < 2.0 ** -9 and abs(float(p[n // 2]) - 0.49) < 2.0 ** -9
+        assert bool((p[-4999:-1] == p[0]).all()) and bool((p[1 << 31:-1] == p[0]).all())
+        if eight:
+            assert bool((scales[0][:-1] == scales[0][0]).all()) and float(scales[0][-1]) == pytest.approx(0.1 / 448, rel=1e-6)
+        else:
+            assert abs(float(m[-1]) + 0.1) < 1e-7 and abs(float(v[n // 2]) - 0.05 * 0.0625) < 1e-8
+        del p, g, m, v

@@ -8,6 +8,9 @@ tg_status xent_forward_bf16(const XentCall& q);
 tg_status xent_backward_f16(const XentCall& q);
 tg_status xent_backward_bf16(const XentCall& q);
 
+// 32-bit offsets within a tile of an operand, as nt_eligible asks
+static bool width_fits(int64_t D, int64_t ld) { return 512 * ld + 2 * D < (int64_t)kNumRecords; }
+
 // what both calls ask of their operands
 static tg_status xent_check(const XentCall& q)
 {
@@ -21,9 +24,7 @@ static tg_status xent_check(const XentCall& q)
             return s;
     if ((uintptr_t)q.target & 7u)
         return TG_ERR_MISALIGNED;
-    // 32-bit offsets within a tile of either operand, as nt_eligible asks
-    const int64_t lim = (int64_t)kNumRecords;
-    if (q.D % 8 != 0 || 512 * q.ldx + 2 * q.D >= lim || 512 * q.ldw + 2 * q.D >= lim)
+    if (q.D % 8 != 0 || !width_fits(q.D, q.ldx) || !width_fits(q.D, q.ldw))
         return TG_ERR_NOT_SUPPORTED;
     return TG_OK;
 }
@@ -38,7 +39,7 @@ extern "C" int64_t tg_linear_xent_workspace_bytes(tg_input in_arg, int64_t M, in
 {
     if (M < 0 || V < 0 || D < 0 || !type_ok(abi_int(in_arg)))
         return -1;
-    if (!dims_fit(M, V, D))
+    if (!dims_fit(M, V, D) || !width_fits(D, D))
         return 0;
     return xent_fwd_layout(M, V, kFusedSkinnyRows<E_BF16>).bytes;
 }
@@ -47,7 +48,7 @@ extern "C" int64_t tg_linear_xent_backward_workspace_bytes(tg_input in_arg, int6
 {
     if (M < 0 || V < 0 || D < 0 || piece < 0 || !type_ok(abi_int(in_arg)))
         return -1;
-    if (V == 0 || !dims_fit(M, V, D))
+    if (V == 0 || !dims_fit(M, V, D) || !width_fits(D, D))
         return 0;
     const int64_t n = xent_bwd_bytes(M, V, D, D, piece);
     return n < 0 ? 0 : n;
