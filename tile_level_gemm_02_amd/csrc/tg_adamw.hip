@@ -6,10 +6,18 @@
 // Bound by memory: every value is read once and written once (fp32 28 bytes a
 // value, bf16 weights and gradients with 8-bit states 10).  Tensors of one
 // combination of types share launches of up to kAdamTensors, whose
-// descriptors travel in the kernel arguments; workgroups walk the tensors'
-// chunks.  A lane takes V consecutive values in 16-byte pieces: 8 with fp32
-// states, 16 with 8-bit ones, where 16 lanes then hold a block of 256 and its
-// largest value is a reduction within a row of lanes.
+// descriptors travel in the kernel arguments; a workgroup takes a chunk.  A
+// lane takes V consecutive values, 4 or 8, so that 64 or 32 lanes hold a block
+// of 8-bit states and its largest value is a reduction between lanes.
+//
+// 300 M bf16 weights with fp32 masters and states 1400 us, 6.0 TB/s; 400 M with
+// 8-bit states 685 us, 5.9 TB/s (a large copy moves 4.75); 9 fp32 tensors of
+// 60 K values 6.8 us.  What got it there: 2048 workgroups that walk the chunks
+// with 32 bytes of each fp32 buffer per lane 2456 and 978 us; one run of whole
+// lines per instruction 1632 and 865; a workgroup for each chunk 1500 and 685;
+// chunks of one unit 1400 with fp32 buffers (two units of 8 values 685, one
+// 692).  Without the non-temporal hint on large loads +3 and +5%, on the
+// stores +4 and +7%.
 #include <math.h>
 
 #include "tg_abi.hpp"
@@ -19,11 +27,15 @@
 namespace tg {
 
 constexpr int kAdamTensors = 48;       // descriptors per launch (under 4 KiB of kernel arguments)
-constexpr int64_t kAdamChunk = 4096;   // elements per chunk
-constexpr int64_t kAdamGrid = 2048;    // workgroups of a launch: 8 per compute unit
+constexpr int64_t kAdamGrid = 1 << 24; // workgroups of a launch at most
 constexpr int kAdamBlock = 256;        // elements per scale of 8-bit states
 constexpr float kE4m3Max = 448.0f, kE4m3Step = 0.001953125f;  // largest and smallest positive value
 constexpr float kAdamTiny = 7.888609052210118e-31f;           // 2^-100
+
+// Values per lane and unit, units per chunk, of a combination of types: see adamw_step
+constexpr int adam_values(bool narrow) { return narrow ? 8 : 4; }
+constexpr int adam_units(bool narrow) { return narrow ? 2 : 1; }
+constexpr int64_t adam_chunk(bool narrow) { return 256 * adam_values(narrow) * adam_units(narrow); }
 
 struct AdamHyper {
     float b1, omb1, b2, omb2;  // omb: 1 - b
@@ -71,65 +83,81 @@ __host__ __device__ inline void adam_constants(AdamHyper& h, int64_t step, doubl
     h.root = (float)(1.0 / __builtin_sqrt(1.0 - beta_power(h.beta2, step)));
 }
 
-// V values of type O from element `e` on, `left` of them there; whole: all are,
-// on a 16-byte boundary.  STREAM: with the non-temporal hint.
-template <int O, int V, bool STREAM>
-__device__ __forceinline__ void load_values(const void* base, int64_t e, int left, bool whole, u32x4* q)
+// W words of a lane from byte `at` on, `left` bytes of them there; whole: all
+// are, on a boundary of their size.  STREAM: with the non-temporal hint.
+template <int W, bool STREAM>
+__device__ __forceinline__ void load_words(const void* base, int64_t at, int left, bool whole, uint32_t* q)
 {
-    constexpr int N = Piece<O>::N;
+    typedef uint32_t vec __attribute__((ext_vector_type(W)));
+    const uint8_t* src = (const uint8_t*)base + at;
     if (whole) {
-        const u32x4* src = (const u32x4*)((const typename OutInfo<O>::T*)base + e);
+        vec v;
+        if constexpr (STREAM)
+            v = __builtin_nontemporal_load((const vec*)src);
+        else
+            v = *(const vec*)src;
 #pragma unroll
-        for (int i = 0; i < V / N; ++i)
-            q[i] = STREAM ? __builtin_nontemporal_load(src + i) : src[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / N; ++i)
-            q[i] = load_piece<O>(base, e + i * N, left - i * N, false);
-    }
-}
-
-template <int O, int V>
-__device__ __forceinline__ void store_values(void* base, int64_t e, int left, bool whole, const float* v)
-{
-    constexpr int N = Piece<O>::N;
-#pragma unroll
-    for (int i = 0; i < V / N; ++i)
-        store_piece<O>(base, e + i * N, pack_piece<O>(v + i * N), left - i * N, whole);
-}
-
-// 16 bytes of e4m3
-template <bool STREAM>
-__device__ __forceinline__ u32x4 load_e4m3(const void* base, int64_t e, int left, bool whole)
-{
-    const uint8_t* src = (const uint8_t*)base + e;
-    if (whole)
-        return STREAM ? __builtin_nontemporal_load((const u32x4*)src) : *(const u32x4*)src;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left)
-            w[i / 4] |= (uint32_t)src[i] << (8 * (i % 4));
-    return u32x4{w[0], w[1], w[2], w[3]};
-}
-
-__device__ __forceinline__ void store_e4m3(void* base, int64_t e, int left, bool whole, u32x4 q)
-{
-    uint8_t* dst = (uint8_t*)base + e;
-    if (whole) {
-        store_nt((u32x4*)dst, q);
+        for (int i = 0; i < W; ++i)
+            q[i] = v[i];
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < W; ++i)
+        q[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 4 * W; ++i)
+        if (i < left)
+            q[i / 4] |= (uint32_t)src[i] << (8 * (i % 4));
+}
+
+template <int W>
+__device__ __forceinline__ void store_words(void* base, int64_t at, int left, bool whole, const uint32_t* q)
+{
+    typedef uint32_t vec __attribute__((ext_vector_type(W)));
+    uint8_t* dst = (uint8_t*)base + at;
+    if (whole) {
+        vec v;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            v[i] = q[i];
+        store_nt((vec*)dst, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * W; ++i)
         if (i < left)
             dst[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
 }
 
-__device__ __forceinline__ void from_e4m3(u32x4 q, float scale, float* v)
+template <int O> struct AdamBytes { static constexpr int N = O == O_F32 ? 4 : 2; };
+
+// value i of words of type O, and V values as such words
+template <int O>
+__device__ __forceinline__ float word_value(const uint32_t* q, int i)
+{
+    if constexpr (O == O_F32)
+        return bit_cast<float>(q[i]);
+    else
+        return piece_value<O>(u32x4{q[i >> 1], 0u, 0u, 0u}, i & 1);
+}
+
+template <int O, int V>
+__device__ __forceinline__ void to_words(const float* v, uint32_t* q)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V * AdamBytes<O>::N / 4; ++i) {
+        if constexpr (O == O_F32)
+            q[i] = bit_cast<uint32_t>(v[i]);
+        else
+            q[i] = pack2<O>(v[2 * i], v[2 * i + 1]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void from_e4m3(const uint32_t* q, float scale, float* v)
+{
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
         const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
         const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
         v[4 * i] = lo[0] * scale;
@@ -139,10 +167,11 @@ __device__ __forceinline__ void from_e4m3(u32x4 q, float scale, float* v)
     }
 }
 
-// largest of the 16 lanes of a row
-__device__ __forceinline__ float row_max(float v)
+// largest of the 32 or 64 lanes that hold a block, in each of them
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v)
 {
-    // row_ror by 8, 4, 2, 1: every lane ends with all 16
+    // within a row of 16 lanes: rotated by 8, 4, 2, 1
 #define TG_ROW_MAX(ctrl) \
     v = __builtin_fmaxf(v, bit_cast<float>(__builtin_amdgcn_mov_dpp(bit_cast<int>(v), ctrl, 0xF, 0xF, true)))
     TG_ROW_MAX(0x128);
@@ -150,24 +179,30 @@ __device__ __forceinline__ float row_max(float v)
     TG_ROW_MAX(0x122);
     TG_ROW_MAX(0x121);
 #undef TG_ROW_MAX
+    // then with the row beside it, and the other half of the wave
+    const auto r = __builtin_amdgcn_permlane16_swap(bit_cast<uint32_t>(v), bit_cast<uint32_t>(v), false, false);
+    v = __builtin_fmaxf(bit_cast<float>((uint32_t)r[0]), bit_cast<float>((uint32_t)r[1]));
+    if constexpr (LANES == 64) {
+        const auto h = __builtin_amdgcn_permlane32_swap(bit_cast<uint32_t>(v), bit_cast<uint32_t>(v), false, false);
+        v = __builtin_fmaxf(bit_cast<float>((uint32_t)h[0]), bit_cast<float>((uint32_t)h[1]));
+    }
     return v;
 }
 
 // A block's values as e4m3 and a scale; LIFT: positive ones stay positive
-template <bool LIFT>
-__device__ __forceinline__ u32x4 to_e4m3(const float* v, float& scale)
+template <int V, bool LIFT>
+__device__ __forceinline__ void to_e4m3(const float* v, uint32_t* q, float& scale)
 {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < V; ++i)
         top = __builtin_fmaxf(top, LIFT ? v[i] : __builtin_fabsf(v[i]));
-    top = row_max(top);
+    top = lanes_max<kAdamBlock / V>(top);
     top = top < kAdamTiny ? 0.0f : top;
     const float inv = top > 0.0f ? kE4m3Max / top : 0.0f;
     scale = top * (1.0f / kE4m3Max);
-    u32x4 q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 4; ++i) {
         float s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -179,7 +214,6 @@ __device__ __forceinline__ u32x4 to_e4m3(const float* v, float& scale)
         w = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], w, true);
         q[i] = (uint32_t)w;
     }
-    return q;
 }
 
 __device__ __forceinline__ int adam_tensor(const AdamArgs& p, uint32_t c)
@@ -196,12 +230,17 @@ __device__ __forceinline__ int adam_tensor(const AdamArgs& p, uint32_t c)
 }
 
 // P: type of the weights, G: of the gradients; MASTER: fp32 weights beside
-// them; EIGHT: 8-bit states
+// them; EIGHT: 8-bit states.  A unit is V consecutive values of a lane, V such
+// that the widest of the buffers takes 16 bytes (and the others less): every
+// load and store of a wave covers one run of whole lines.
 template <int P, int G, bool MASTER, bool EIGHT, bool STREAM>
 __global__ __launch_bounds__(256) void adamw_step(AdamArgs a)
 {
     static_assert(!MASTER || P != O_F32, "masters of 16-bit weights");
-    constexpr int V = EIGHT ? 16 : 8, WT = MASTER ? (int)O_F32 : P;
+    constexpr int WT = MASTER ? (int)O_F32 : P;
+    constexpr bool NARROW = WT != O_F32 && G != O_F32 && EIGHT;  // nothing of 32 bits
+    constexpr int V = adam_values(NARROW), UNITS = adam_units(NARROW);
+    constexpr int PW = V * AdamBytes<P>::N / 4, GW = V * AdamBytes<G>::N / 4, WW = V * AdamBytes<WT>::N / 4, SW = EIGHT ? V / 4 : V;
     AdamHyper h = a.h;
     float coef = 1.0f;
     if (h.norm != nullptr) {
@@ -215,70 +254,88 @@ __global__ __launch_bounds__(256) void adamw_step(AdamArgs a)
     const uint32_t chunks = a.first[a.count], tid = threadIdx.x;
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int t = adam_tensor(a, c);
-        const int64_t c0 = (int64_t)(c - a.first[t]) * kAdamChunk, n = a.n[t];
+        const int64_t c0 = (int64_t)(c - a.first[t]) * adam_chunk(NARROW) + tid * V, n = a.n[t];
         const bool aligned = a.aligned[t] != 0;
+        uint32_t gq[UNITS][GW], wq[UNITS][WW], mq[UNITS][SW], vq[UNITS][SW];
+        float sm[UNITS], sv[UNITS];
+        auto values_left = [&](int u) __attribute__((always_inline)) -> int {
+            const int64_t rest = n - (c0 + (int64_t)u * 256 * V);
+            return rest >= V ? V : rest > 0 ? (int)rest : 0;
+        };
 #pragma unroll
-        for (int k = 0; k < (int)kAdamChunk / (256 * V); ++k) {
-            const int64_t e0 = c0 + (int64_t)k * 256 * V + tid * V, rest = n - e0;
-            const int left = rest >= V ? V : rest > 0 ? (int)rest : 0;
+        for (int u = 0; u < UNITS; ++u) {
+            const int64_t e = c0 + (int64_t)u * 256 * V;
+            const int left = values_left(u);
             const bool whole = aligned && left == V;
-            u32x4 gq[V / Piece<G>::N], wq[V / Piece<WT>::N], mq[EIGHT ? 1 : V / 4], vq[EIGHT ? 1 : V / 4];
-            float w[V], m[V], v[V], r[V];
             if (left > 0) {
-                load_values<G, V, STREAM>(a.g[t], e0, left, whole, gq);
-                load_values<WT, V, STREAM>(MASTER ? (const void*)a.w[t] : a.p[t], e0, left, whole, wq);
+                constexpr int S = EIGHT ? 1 : 4;
+                load_words<GW, STREAM>(a.g[t], e * AdamBytes<G>::N, left * AdamBytes<G>::N, whole, gq[u]);
+                load_words<WW, STREAM>(MASTER ? (const void*)a.w[t] : a.p[t], e * AdamBytes<WT>::N, left * AdamBytes<WT>::N, whole, wq[u]);
+                load_words<SW, STREAM>(a.m[t], e * S, left * S, whole, mq[u]);
+                load_words<SW, STREAM>(a.v[t], e * S, left * S, whole, vq[u]);
                 if constexpr (EIGHT) {
-                    mq[0] = load_e4m3<STREAM>(a.m[t], e0, left, whole);
-                    vq[0] = load_e4m3<STREAM>(a.v[t], e0, left, whole);
-                    from_e4m3(mq[0], a.sm[t][e0 / kAdamBlock], m);
-                    from_e4m3(vq[0], a.sv[t][e0 / kAdamBlock], v);
-                } else {
-                    load_values<O_F32, V, STREAM>(a.m[t], e0, left, whole, mq);
-                    load_values<O_F32, V, STREAM>(a.v[t], e0, left, whole, vq);
+                    sm[u] = a.sm[t][e / kAdamBlock];
+                    sv[u] = a.sv[t][e / kAdamBlock];
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    w[i] = m[i] = v[i] = r[i] = 0.0f;
             }
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int64_t e = c0 + (int64_t)u * 256 * V;
+            const int left = values_left(u);
+            const bool whole = aligned && left == V;
+            float w[V], m[V], v[V], r[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                m[i] = r[i] = 0.0f;
             if (left > 0) {
+                if constexpr (EIGHT) {
+                    from_e4m3<V>(mq[u], sm[u], m);
+                    from_e4m3<V>(vq[u], sv[u], v);
+                }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float g = piece_value<G>(gq[i / Piece<G>::N], i % Piece<G>::N) * coef;
-                    const float w0 = piece_value<WT>(wq[i / Piece<WT>::N], i % Piece<WT>::N);
-                    const float m0 = EIGHT ? m[i] : piece_value<O_F32>(mq[EIGHT ? 0 : i / 4], i % 4);
-                    const float v0 = EIGHT ? v[i] * v[i] : piece_value<O_F32>(vq[EIGHT ? 0 : i / 4], i % 4);
+                    const float g = word_value<G>(gq[u], i) * coef;
+                    const float w0 = word_value<WT>(wq[u], i);
+                    const float m0 = EIGHT ? m[i] : bit_cast<float>(mq[u][EIGHT ? 0 : i]);
+                    const float v0 = EIGHT ? v[i] * v[i] : bit_cast<float>(vq[u][EIGHT ? 0 : i]);
                     m[i] = m0 * h.b1 + g * h.omb1;
                     v[i] = v0 * h.b2 + g * h.omb2 * g;
                     r[i] = __builtin_amdgcn_sqrtf(v[i]);
                     w[i] = w0 * h.decay - m[i] * __builtin_amdgcn_rcpf(r[i] * h.root + h.eps) * h.step_size;
                 }
-                if constexpr (EIGHT) {
-                    // (values past the tensor's end: out of the block's largest)
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (i >= left)
-                            m[i] = r[i] = 0.0f;
+                uint32_t q[V];
+                to_words<P, V>(w, q);
+                store_words<PW>(a.p[t], e * AdamBytes<P>::N, left * AdamBytes<P>::N, whole, q);
+                if constexpr (MASTER) {
+                    to_words<O_F32, V>(w, q);
+                    store_words<V>(a.w[t], e * 4, left * 4, whole, q);
                 }
-                store_values<P, V>(a.p[t], e0, left, whole, w);
-                if constexpr (MASTER)
-                    store_values<O_F32, V>(a.w[t], e0, left, whole, w);
             }
             if constexpr (EIGHT) {
-                // (every lane of the row takes part)
-                float sm, sv;
-                const u32x4 qm = to_e4m3<false>(m, sm), qv = to_e4m3<true>(r, sv);
+                // (values past the tensor's end stay out of the block's largest; every lane of the block takes part)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i >= left)
+                        m[i] = r[i] = 0.0f;
+                uint32_t qm[V / 4], qv[V / 4];
+                float nm, nv;
+                to_e4m3<V, false>(m, qm, nm);
+                to_e4m3<V, true>(r, qv, nv);
                 if (left > 0) {
-                    store_e4m3(a.m[t], e0, left, whole, qm);
-                    store_e4m3(a.v[t], e0, left, whole, qv);
-                    if (e0 % kAdamBlock == 0) {
-                        a.sm[t][e0 / kAdamBlock] = sm;
-                        a.sv[t][e0 / kAdamBlock] = sv;
+                    store_words<V / 4>(a.m[t], e, left, whole, qm);
+                    store_words<V / 4>(a.v[t], e, left, whole, qv);
+                    if (e % kAdamBlock == 0) {
+                        a.sm[t][e / kAdamBlock] = nm;
+                        a.sv[t][e / kAdamBlock] = nv;
                     }
                 }
             } else if (left > 0) {
-                store_values<O_F32, V>(a.m[t], e0, left, whole, m);
-                store_values<O_F32, V>(a.v[t], e0, left, whole, v);
+                uint32_t q[V];
+                to_words<O_F32, V>(m, q);
+                store_words<V>(a.m[t], e * 4, left * 4, whole, q);
+                to_words<O_F32, V>(v, q);
+                store_words<V>(a.v[t], e * 4, left * 4, whole, q);
             }
         }
     }
@@ -376,6 +433,7 @@ extern "C" tg_status tg_adamw(int64_t count, const tg_adamw_tensor* tensors, int
     for (int kind = 0; kind < 18; ++kind) {  // (masters of fp32 weights: none)
         const int p = kind / 6, g = kind / 2 % 3;
         const bool master = kind % 2 != 0;
+        const int64_t chunk = adam_chunk(eight && p != TG_F32 && g != TG_F32 && !master);
         for (int64_t i = 0; i < count;) {
             int64_t chunks = 0;
             a.count = 0;
@@ -383,7 +441,7 @@ extern "C" tg_status tg_adamw(int64_t count, const tg_adamw_tensor* tensors, int
                 const tg_adamw_tensor& t = tensors[i];
                 if (t.n == 0 || t.p_dtype != p || t.g_dtype != g || (t.master != nullptr) != master)
                     continue;
-                const int64_t c = (t.n + kAdamChunk - 1) / kAdamChunk;
+                const int64_t c = (t.n + chunk - 1) / chunk;
                 if (chunks + c > 0xFFFFFFFF)
                     break;
                 const int k = a.count++;
