@@ -198,6 +198,41 @@ def test_residual_in_place_empty_and_repeated(tg, ws):
     assert bool((s == 0).all())
 
 
+def test_wrong_tensors_are_refused(tg, ws):
+    z = lambda *s, dtype=F32: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
+    x, w, y, sx, sw = z(4, 32, dtype=I8), z(8, 32, dtype=I8), z(4, 8), z(4), z(8)
+
+    def no(match, fn, *a, **k):
+        with pytest.raises(ValueError, match=match):
+            fn(*a, **k)
+
+    q = tg.tg_quantize_i8
+    no("float32, float16 or bfloat16", q, x, x, sx)
+    no("q must be int8", q, z(4, 32), z(4, 32), sx)
+    no("q must be 4x32", q, z(4, 32), x[:, :16], sx)
+    no("scale must be", q, z(4, 32), x, sw)
+    no("2-D", q, z(32), x, sx)
+    no("unit stride", q, z(32, 4).t(), x, sx)
+    no("not", q, z(4, 32), x.cpu(), sx)
+    f = tg.tg_linear_i8
+    no("x must be int8", f, x.float(), w, y, sx, sw)
+    no("W must be int8", f, x, w.float(), y, sx, sw)
+    no("W must be 8x32", f, x, w[:, :16], y, sx, sw)
+    no("Y must be 4x8", f, x, w, y[:3], sx, sw)
+    no("Y must be float32", f, x, w, y.double(), sx, sw)
+    no("scale_x", f, x, w, y, sw, sw)
+    no("scale_w", f, x, w, y, sx, sw.half())
+    no("bias", f, x, w, y, sx, sw, bias=sx)
+    no("residual must be of Y", f, x, w, y, sx, sw, residual=y.half())
+    no("residual must be 4x8", f, x, w, y, sx, sw, residual=y[:2])
+    no("activation", f, x, w, y, sx, sw, act="tanh")
+    no("workspace", f, x, w, y, sx, sw, workspace=torch.zeros(8, dtype=torch.int32))
+    with pytest.raises(tg.TGError):
+        f(x[:, :24], w[:, :24], y, sx, sw)  # K not a multiple of 16
+    with pytest.raises(tg.TGError):
+        f(x, w, z(4, 9)[:, 1:], sx, sw)  # not aligned
+
+
 def test_captured_and_on_another_stream(tg):
     """Quantization and product captured, and replayed on new activations between eager calls; K split in both."""
     M, N, K = 100, 520, 8192

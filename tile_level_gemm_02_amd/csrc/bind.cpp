@@ -1,7 +1,8 @@
-// Marshalling of tg_clip_grads and tg_adamw for Python: reads the tensors of a
-// list (their types, sizes, devices and pointers) in C++.  Read one attribute at
-// a time from Python they take about 0.5 us each tensor, 72 us for 56 gradients
-// with their outputs, several times the kernels of a small call.
+// Marshalling of tg_clip_grads, tg_adamw and the int8 layers for Python: reads
+// the tensors (their types, sizes, devices and pointers) in C++.  Read one
+// attribute at a time from Python they take about 0.5 us each tensor, 72 us for
+// 56 gradients with their outputs, several times the kernels of a small call; a
+// token through an int8 layer is 8 us of kernels and was 14 of marshalling.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -9,6 +10,7 @@
 
 #include <vector>
 
+#include "tg_int8.h"
 #include "tg_ops.h"
 #include "tg_train.h"
 
@@ -98,12 +100,8 @@ PyObject* clip_grads(PyObject*, PyObject* args)
     }
 }
 
-// C type of a float tensor, or -1
-int dtype_of(const at::Tensor& t)
-{
-    const auto s = t.scalar_type();
-    return s == at::kFloat ? TG_F32 : s == at::kHalf ? TG_F16 : s == at::kBFloat16 ? TG_BF16 : -1;
-}
+// tg_dtype of an element type, or -1
+int c_dtype(at::ScalarType s) { return s == at::kFloat ? TG_F32 : s == at::kHalf ? TG_F16 : s == at::kBFloat16 ? TG_BF16 : -1; }
 
 // a tensor of one element of type `type` on GPU `dev`: its pointer, else null with an error set
 const void* scalar_on(PyObject* o, int64_t dev, at::ScalarType type, const char* what)
@@ -155,7 +153,7 @@ PyObject* adamw(PyObject*, PyObject* args)
                 if (x == nullptr)
                     return nullptr;
                 if (k < 2) {
-                    type[k] = dtype_of(*x);
+                    type[k] = c_dtype(x->scalar_type());
                     if (type[k] < 0)
                         return refuse("params and grads must be float32, float16 or bfloat16");
                 } else if (x->scalar_type() != (eight && k < 4 ? at::kFloat8_e4m3fn : at::kFloat)) {
@@ -202,8 +200,154 @@ PyObject* adamw(PyObject*, PyObject* args)
     }
 }
 
+// A matrix argument: the strides and devices that ops.py's _mat takes
+struct Mat {
+    void* p = nullptr;
+    int64_t rows = 0, cols = 0, ld = 0;
+    at::ScalarType type = at::kFloat;
+};
+
+bool matrix(PyObject* o, const char* name, int64_t dev, Mat& m)
+{
+    if (!THPVariable_Check(o)) {
+        PyErr_Format(PyExc_ValueError, "%s must be a tensor", name);
+        return false;
+    }
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.dim() != 2) {
+        PyErr_Format(PyExc_ValueError, "%s must be 2-D", name);
+        return false;
+    }
+    m.rows = t.size(0);
+    m.cols = t.size(1);
+    m.type = t.scalar_type();
+    if (t.stride(1) != 1 && m.cols > 1) {
+        PyErr_Format(PyExc_ValueError, "%s must have unit stride along its last dimension", name);
+        return false;
+    }
+    if (!t.is_cuda() || t.get_device() != dev) {
+        PyErr_Format(PyExc_ValueError, "every tensor must be on the current GPU, %s is not", name);
+        return false;
+    }
+    // one row has no second one: its stride is not looked at, an aligned one stands for it
+    m.ld = m.rows > 1 ? t.stride(0) : (m.cols + 15) & -16;
+    m.p = t.data_ptr();
+    return true;
+}
+
+bool shaped(const Mat& m, const char* name, int64_t rows, int64_t cols)
+{
+    if (m.rows == rows && m.cols == cols)
+        return true;
+    PyErr_Format(PyExc_ValueError, "%s must be %lldx%lld, got %lldx%lld", name, (long long)rows, (long long)cols, (long long)m.rows,
+                 (long long)m.cols);
+    return false;
+}
+
+bool typed(const Mat& m, const char* name, at::ScalarType type, const char* what)
+{
+    if (m.type == type)
+        return true;
+    PyErr_Format(PyExc_ValueError, "%s must be %s", name, what);
+    return false;
+}
+
+// a contiguous float32 vector of n
+bool vector(PyObject* o, const char* name, int64_t n, int64_t dev, float*& p)
+{
+    if (THPVariable_Check(o)) {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (t.scalar_type() == at::kFloat && t.dim() == 1 && t.size(0) == n && t.is_contiguous()) {
+            if (!t.is_cuda() || t.get_device() != dev) {
+                PyErr_Format(PyExc_ValueError, "every tensor must be on the current GPU, %s is not", name);
+                return false;
+            }
+            p = (float*)t.data_ptr();
+            return true;
+        }
+    }
+    PyErr_Format(PyExc_ValueError, "%s must be a contiguous float32 vector of %lld", name, (long long)n);
+    return false;
+}
+
+typedef tg_status (*quantize_fn)(int, int64_t, int64_t, const void*, int64_t, int8_t*, int64_t, float*, void*);
+
+// quantize_i8(function address, x, q, scale, device index, stream) -> status
+PyObject* quantize_i8(PyObject*, PyObject* args)
+{
+    unsigned long long fn, stream;
+    PyObject *x_o, *q_o, *scale_o;
+    long long dev;
+    if (!PyArg_ParseTuple(args, "KOOOLK", &fn, &x_o, &q_o, &scale_o, &dev, &stream))
+        return nullptr;
+    try {
+        Mat x, q;
+        float* scale = nullptr;
+        if (!matrix(x_o, "x", dev, x))
+            return nullptr;
+        if (c_dtype(x.type) < 0)
+            return refuse("x must be float32, float16 or bfloat16");
+        if (!matrix(q_o, "q", dev, q) || !typed(q, "q", at::kChar, "int8") || !shaped(q, "q", x.rows, x.cols) ||
+            !vector(scale_o, "scale", x.rows, dev, scale))
+            return nullptr;
+        return PyLong_FromLong((long)((quantize_fn)(uintptr_t)fn)(c_dtype(x.type), x.rows, x.cols, x.p, x.ld, (int8_t*)q.p, q.ld, scale,
+                                                                  (void*)(uintptr_t)stream));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+typedef tg_status (*linear_i8_fn)(int64_t, int64_t, int64_t, const int8_t*, int64_t, const int8_t*, int64_t, const float*, const float*,
+                                  const float*, int, const void*, int64_t, void*, int64_t, int, void*, int64_t, void*);
+
+// linear_i8(function address, x, W, Y, scale_x, scale_w, bias or None, act, residual or None, workspace or None, device index,
+//           stream) -> status
+PyObject* linear_i8(PyObject*, PyObject* args)
+{
+    unsigned long long fn, stream;
+    PyObject *x_o, *w_o, *y_o, *sx_o, *sw_o, *b_o, *r_o, *ws_o;
+    int act;
+    long long dev;
+    if (!PyArg_ParseTuple(args, "KOOOOOOiOOLK", &fn, &x_o, &w_o, &y_o, &sx_o, &sw_o, &b_o, &act, &r_o, &ws_o, &dev, &stream))
+        return nullptr;
+    try {
+        Mat x, w, y, r;
+        float *sx = nullptr, *sw = nullptr, *b = nullptr;
+        if (!matrix(x_o, "x", dev, x) || !typed(x, "x", at::kChar, "int8") || !matrix(w_o, "W", dev, w) ||
+            !typed(w, "W", at::kChar, "int8") || !shaped(w, "W", w.rows, x.cols) || !matrix(y_o, "Y", dev, y) ||
+            !shaped(y, "Y", x.rows, w.rows))
+            return nullptr;
+        if (c_dtype(y.type) < 0)
+            return refuse("Y must be float32, float16 or bfloat16");
+        if (!vector(sx_o, "scale_x", x.rows, dev, sx) || !vector(sw_o, "scale_w", w.rows, dev, sw) ||
+            (b_o != Py_None && !vector(b_o, "bias", w.rows, dev, b)))
+            return nullptr;
+        if (r_o != Py_None && (!matrix(r_o, "residual", dev, r) || !typed(r, "residual", y.type, "of Y's type") ||
+                               !shaped(r, "residual", x.rows, w.rows)))
+            return nullptr;
+        void* ws = nullptr;
+        int64_t ws_bytes = 0;
+        if (ws_o != Py_None) {
+            const at::Tensor* t = contiguous_on(ws_o, dev, "the workspace");
+            if (t == nullptr)
+                return nullptr;
+            ws = t->data_ptr();
+            ws_bytes = (int64_t)t->nbytes();
+        }
+        return PyLong_FromLong((long)((linear_i8_fn)(uintptr_t)fn)(x.rows, w.rows, x.cols, (const int8_t*)x.p, x.ld, (const int8_t*)w.p, w.ld,
+                                                                   sx, sw, b, act, r.p, r.ld, y.p, y.ld, c_dtype(y.type), ws, ws_bytes,
+                                                                   (void*)(uintptr_t)stream));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 PyMethodDef methods[] = {{"clip_grads", clip_grads, METH_VARARGS, "Marshals a tg_clip_grads call; returns its status."},
                          {"adamw", adamw, METH_VARARGS, "Marshals a tg_adamw call; returns its status."},
+                         {"quantize_i8", quantize_i8, METH_VARARGS, "Marshals a tg_quantize_i8 call; returns its status."},
+                         {"linear_i8", linear_i8, METH_VARARGS, "Marshals a tg_linear_i8 call; returns its status."},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tgbind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

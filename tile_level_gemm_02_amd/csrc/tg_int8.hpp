@@ -122,26 +122,51 @@ struct I8SkinnyArgs : SkinnyArgs {
     }
 };
 
-// Rows up to which a call takes the skinny kernel
+// Rows up to which a call takes the skinny kernel (33 rows, N = K = 8192: 15.9
+// us on the tile kernel with K split; 32 rows 14.2 here, 15.9 there)
 constexpr int64_t kI8SkinnyRows = 32;
 
-template <int O, int AI, int SPLIT, int CG>
+template <int O, int WAVES, int RING, int AI, int SPLIT, int CG>
 void launch_i8_skinny(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipStream_t s)
 {
-    typedef SkinnyCfg G;
-    hipLaunchKernelGGL((skinny_gemm<E_I8, O, G::WAVES, AI, G::RING, SPLIT, CG, EPI_OWN, I8SkinnyArgs<O>>),
-                       dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * G::WAVES), 0, s, a);
+    hipLaunchKernelGGL((skinny_gemm<E_I8, O, WAVES, AI, RING, SPLIT, CG, EPI_OWN, I8SkinnyArgs<O>>),
+                       dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * WAVES), 0, s, a);
 }
 
-template <int O, int SPLIT>
+constexpr int kI8MostRing = 4;
+
+// Waves per workgroup and ring slots per wave of the skinny kernel.  An int8
+// row is half the bytes of a 16-bit one, so eight waves get few stages each:
+// four waves with a deeper ring stream faster wherever a workgroup's K is all
+// that a compute unit reads (up to 256 workgroups), and what counts past that is
+// how many workgroups a unit's LDS holds (three slots, and two for several
+// slices of rows).  Back to back, three weights in turn, us:
+//                      8 waves, 2   4 waves, 4   4 waves, 3   4 waves, 2
+//    1 x  4096 x 4096      5.4          5.2          5.4          6.0
+//    1 x  1024 x 4096      3.9          4.5          4.4          4.4
+//   16 x  8192 x 8192     14.9         13.4         13.4         13.5
+//   16 x  8200 x 8192     20.0         19.1         16.6         16.4
+//   32 x  8192 x 8192     17.7         16.8         14.1         14.2
+//   24 x  8200 x 8192     21.1         21.4         17.6         15.9
+//   20 x 10240 x 4096       -          16.7         13.0         11.5
+template <int O>
 void launch_i8_rows(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipStream_t s)
 {
-    if (a.M <= 8)
-        launch_i8_skinny<O, 1, SPLIT, 1>(a, blocks, split, s);
-    else if (fused_cg(a.M, a.N) == 1)
-        launch_i8_skinny<O, 2, SPLIT, 1>(a, blocks, split, s);
-    else
-        launch_i8_skinny<O, 2, SPLIT, 2>(a, blocks, split, s);
+    const bool one = a.M <= 8, wide = fused_cg(a.M, a.N) == 2;
+    if (a.M > 16) {
+        split > 1 ? launch_i8_skinny<O, 4, 2, 2, 2, 2>(a, blocks, split, s) : launch_i8_skinny<O, 4, 2, 2, 0, 2>(a, blocks, 1, s);
+    } else if (blocks <= 128) {  // (the only ones split)
+        if (split > 1)
+            one ? launch_i8_skinny<O, 8, 2, 1, 2, 1>(a, blocks, split, s) : launch_i8_skinny<O, 8, 2, 2, 2, 1>(a, blocks, split, s);
+        else
+            one ? launch_i8_skinny<O, 8, 2, 1, 0, 1>(a, blocks, 1, s) : launch_i8_skinny<O, 8, 2, 2, 0, 1>(a, blocks, 1, s);
+    } else if (blocks <= 256 && !wide) {
+        one ? launch_i8_skinny<O, 4, 4, 1, 0, 1>(a, blocks, 1, s) : launch_i8_skinny<O, 4, 4, 2, 0, 1>(a, blocks, 1, s);
+    } else if (wide) {
+        launch_i8_skinny<O, 4, 3, 2, 0, 2>(a, blocks, 1, s);
+    } else {
+        one ? launch_i8_skinny<O, 4, 3, 1, 0, 1>(a, blocks, 1, s) : launch_i8_skinny<O, 4, 3, 2, 0, 1>(a, blocks, 1, s);
+    }
 }
 
 inline int64_t i8_ws_bytes(int64_t M, int64_t N, int64_t K)
@@ -158,7 +183,7 @@ inline int64_t i8_ws_bytes(int64_t M, int64_t N, int64_t K)
 template <int O>
 tg_status i8_linear(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_bytes, hipStream_t s)
 {
-    if (t.M <= kI8SkinnyRows && t.K > 0 && skinny_offsets_fit(t.K, t.lda, t.ldb, SkinnyCfg::RING, fused_cg(t.M, t.N))) {
+    if (t.M <= kI8SkinnyRows && t.K > 0 && skinny_offsets_fit(t.K, t.lda, t.ldb, kI8MostRing, fused_cg(t.M, t.N))) {
         I8SkinnyArgs<O> a{};
         a.M = t.M;
         a.N = t.N;
@@ -173,15 +198,15 @@ tg_status i8_linear(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_byte
         const int64_t blocks = fused_skinny_blocks(a.M, a.N);
         if (blocks > 0x7FFFFFFF)
             return TG_ERR_NOT_SUPPORTED;
-        const int split = fused_split<E_I8>(blocks, a.K);
+        int split = fused_split<E_I8>(blocks, a.K);
         const int64_t need = fused_skinny_ws_bytes(a.M, a.N, blocks, split);
-        if (ws != nullptr && need > 0 && need <= ws_bytes) {
+        if (ws == nullptr || need == 0 || need > ws_bytes)
+            split = 1;
+        if (split > 1) {
             a.counters = (uint32_t*)ws;
             a.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
-            launch_i8_rows<O, 2>(a, blocks, split, s);
-        } else {
-            launch_i8_rows<O, 0>(a, blocks, 1, s);
         }
+        launch_i8_rows(a, blocks, split, s);
         return launched();
     }
     I8Args<O> a{};

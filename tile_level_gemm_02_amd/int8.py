@@ -12,21 +12,19 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
-from . import _CDTYPE, TGError, _stream, load
-from .ops import _2d, _NONE, _OWN, _act, _current_stream, _device, _mat, _vec, _ws
+from . import TGError, _stream, load
+from . import ops as _ops
+from .ops import _act, _current_stream, _device
 
 EXPORTS = ("tg_quantize_i8", "tg_linear_i8", "tg_linear_i8_workspace_bytes")
 
 _fns = None
-_I8 = (torch.int8,)
-_FLOATS = tuple(_CDTYPE)
+_quantize_address = _linear_address = 0  # in the loaded library
 
 
 def _lib():
     """The library with the argument types of these entry points set."""
-    global _fns
+    global _fns, _quantize_address, _linear_address
     if _fns is None:
         lib = load()
         i64, vp, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
@@ -36,19 +34,25 @@ def _lib():
         lib.tg_quantize_i8.restype = lib.tg_linear_i8.restype = ci
         lib.tg_linear_i8_workspace_bytes.argtypes = [i64, i64, i64]
         lib.tg_linear_i8_workspace_bytes.restype = i64
+        _quantize_address = ctypes.cast(lib.tg_quantize_i8, ctypes.c_void_p).value
+        _linear_address = ctypes.cast(lib.tg_linear_i8, ctypes.c_void_p).value
         _fns = lib
     return _fns
 
 
+def _bind():
+    """The native helper, which reads the tensors of these calls."""
+    if _fns is None:
+        _lib()
+    if _ops._bind is None:
+        _ops._load_bind()
+    return _ops._bind
+
+
 def tg_quantize_i8(x, q, scale, stream=None) -> None:
     """q = round(x / scale) as int8 with scale[m] = max |x[m]| / 127: tokens of activations, or channels of a weight."""
-    M, K = _2d(x, "x")
     dev = _device(x, "x")
-    px, ldx = _mat(x, "x", M, K, _FLOATS, dev)
-    pq, ldq = _mat(q, "q", M, K, _I8, dev)
-    ps = _vec(scale, "scale", M, dev)
-    code = (_fns or _lib()).tg_quantize_i8(_CDTYPE[x.dtype], M, K, px, ldx, pq, ldq, ps,
-                                           _current_stream(dev) if stream is None else _stream(stream))
+    code = _bind().quantize_i8(_quantize_address, x, q, scale, dev, _current_stream(dev) if stream is None else _stream(stream))
     if code:
         raise TGError("tg_quantize_i8", code)
 
@@ -63,19 +67,9 @@ def tg_linear_i8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def tg_linear_i8(x, W, Y, scale_x, scale_w, bias=None, act: str = "none", residual=None, workspace=None, stream=None) -> None:
     """Y = act(scale_x[m] scale_w[n] (x . W^T) + bias) + residual, x and W int8 (W stored N x K), the sums exact."""
-    M, K = _2d(x, "x")
-    N = _2d(W, "W")[0]
     a = _act(act)
     dev = _device(x, "x")
-    px, ldx = _mat(x, "x", M, K, _I8, dev)
-    pw, ldw = _mat(W, "W", N, K, _I8, dev)
-    py, ldy = _mat(Y, "Y", M, N, _FLOATS, dev)
-    yt = Y.dtype
-    pr, ldr = _NONE if residual is None else _mat(residual, "residual", M, N, _OWN[yt], dev)
-    sx, sw = _vec(scale_x, "scale_x", M, dev), _vec(scale_w, "scale_w", N, dev)
-    pb = None if bias is None else _vec(bias, "bias", N, dev)
-    ps, ns = _ws(workspace, dev)
-    code = (_fns or _lib()).tg_linear_i8(M, N, K, px, ldx, pw, ldw, sx, sw, pb, a, pr, ldr, py, ldy, _CDTYPE[yt], ps, ns,
-                                         _current_stream(dev) if stream is None else _stream(stream))
+    code = _bind().linear_i8(_linear_address, x, W, Y, scale_x, scale_w, bias, a, residual, workspace, dev,
+                             _current_stream(dev) if stream is None else _stream(stream))
     if code:
         raise TGError("tg_linear_i8", code)
