@@ -29,6 +29,14 @@ struct FxArgs : TileArgs {
     static constexpr EpiArgs e{};
 };
 
+// Arguments whose K split leaves its partial tiles in the workspace for a
+// kernel of its own to add (with many splits the last arrival's adding, one
+// compute unit for a whole tile, would take longer than the product).
+// Workgroup (tile, split) writes f32x4 number b 64 + lane of wave w at
+// ((tile S + split) 8 + w) 8192 floats: rows 16 (b / 4) + lane % 16 and columns
+// 16 (b % 4) + 4 (lane / 16) .. +3 of the wave's 128 x 64.
+struct KeepsPartials {};
+
 template <int E, int O, int NH, int AL, int BL, int EPI, class P>
 __global__ __launch_bounds__(512) void gemm_fx(P p)
 {
@@ -306,12 +314,21 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
         wait_copies<0>();  // copies past the last step (zeros) must land before LDS is reused
     };
     if (NK > 0) {
-        if (rows_a == BM && rows_b == BNO && K % KE == 0)  // full tiles, no K tail
+        const bool tail = K % KE != 0 && (!std::is_base_of<KeepsPartials, P>::value || kt0 + NK == KT);
+        if (rows_a == BM && rows_b == BNO && !tail)  // full tiles, no K tail
             run(std::false_type{});
         else
             run(std::true_type{});
     }
     mfma_drain();
+    if constexpr (std::is_base_of<KeepsPartials, P>::value) {
+        float* const share = p.partials + (((size_t)stile * S + ks) * NW + wave) * 8192;
+#pragma unroll
+        for (int b = 0; b < 32; ++b)
+            if (m0 + wm * 128 + b / 4 * 16 < M)  // (rows past the last are not read)
+                *(f32x4*)(share + (b * 64 + lane) * 4) = acc[b / 4][b % 4];
+        return;
+    }
     __syncthreads();  // the epilogue reuses the stage buffers
 
     // ---- K split: as gemm_nt's for tiles of many blocks (the own share is

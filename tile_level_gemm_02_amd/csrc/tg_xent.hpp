@@ -167,13 +167,13 @@ __device__ __forceinline__ void join_pair(float& top, float& sum, float t, float
 }
 
 // The slots of R rows per workgroup, 256 / R lanes to a row, several loads
-// ahead of their arithmetic.  Each lane's slots, and then the lanes, are added
-// in a fixed order.
+// ahead of their arithmetic; lanes and waves are added in a fixed order.  Bound
+// by the slots' reads (8 bytes for every 64 columns of every row).
 template <int R>
 __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
 {
     constexpr int T = 256 / R, B = 8;
-    __shared__ float red[2][T][R];
+    __shared__ float red[2][4][R];
     __shared__ double own[2][R];
     __shared__ bool last;
     const uint32_t tid = threadIdx.x, r = tid % R, part = tid / R;
@@ -201,22 +201,26 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
             join_pair(top, sum, m, s);
         }
     }
-    red[0][part][r] = top;
-    red[1][part][r] = sum;
-    __syncthreads();
-    if constexpr (T > 64) {  // (one row: 256 lanes' pairs become 64)
-        if (tid < 64u) {
+    // the lanes of a wave that share a row, then the waves: first the largest,
+    // then the sums relative to it
+    float most = top;
 #pragma unroll
-            for (int k = 1; k < T / 64; ++k)
-                join_pair(top, sum, red[0][part + 64 * k][r], red[1][part + 64 * k][r]);
+    for (int d = 32; d >= R; d >>= 1)
+        most = max2(most, __shfl_xor(most, d, 64));
+    sum *= __builtin_amdgcn_exp2f(top - reference_of(most));
 #pragma unroll
-            for (int d = 32; d > 0; d >>= 1)
-                join_pair(top, sum, __shfl_xor(top, d, 64), __shfl_xor(sum, d, 64));
-        }
-    } else if (tid < (uint32_t)R) {
-        for (int k = 1; k < T; ++k)
-            join_pair(top, sum, red[0][k][r], red[1][k][r]);
+    for (int d = 32; d >= R; d >>= 1)
+        sum += __shfl_xor(sum, d, 64);
+    top = most;
+    if (tid % 64u < (uint32_t)R) {
+        red[0][tid / 64u][r] = top;
+        red[1][tid / 64u][r] = sum;
     }
+    __syncthreads();
+    if (tid < (uint32_t)R)
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            join_pair(top, sum, red[0][k][r], red[1][k][r]);
     if (tid < (uint32_t)R) {
         double counted = 0.0, mine = 0.0;
         if (row < p.M) {
@@ -238,7 +242,8 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
     }
     if (p.total == nullptr)
         return;
-    // this workgroup's sums into its slot; the last to arrive adds all slots in order
+    // this workgroup's sums into its slot; the last to arrive adds all slots, in
+    // an order that does not depend on which it is
     __syncthreads();
     if (tid == 0u) {
         double a = 0.0, b = 0.0;
@@ -252,22 +257,19 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
         last = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1u;
     }
     __syncthreads();
-    if (!last)
+    if (!last || tid >= 64u)
         return;
-    __shared__ double all[2][256];
     double a = 0.0, b = 0.0;
-    for (uint32_t k = tid; k < gridDim.x; k += 256u) {
+    for (uint32_t k = tid; k < gridDim.x; k += 64u) {
         a += __hip_atomic_load(p.sums + 2 * (size_t)k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         b += __hip_atomic_load(p.sums + 2 * (size_t)k + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    all[0][tid] = a;
-    all[1][tid] = b;
-    __syncthreads();
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        a += __shfl_down(a, d, 64);
+        b += __shfl_down(b, d, 64);
+    }
     if (tid == 0u) {
-        for (int k = 1; k < 256; ++k) {
-            a += all[0][k];
-            b += all[1][k];
-        }
         __hip_atomic_exchange(p.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         p.total[0] = (float)a;
         p.total[1] = (float)b;
@@ -367,6 +369,68 @@ struct XentProdArgs : TileArgs {
             });
     }
 };
+
+// dX's product with its K, a piece of the vocabulary, split over workgroups:
+// it has few tiles and a long K
+struct XentPartArgs : TileArgs, KeepsPartials {
+    template <int RBK, int WR, int WC, int PBY, class Get>
+    __device__ __forceinline__ void finish(uint8_t*, uint32_t, int64_t, int64_t, Get) const {}  // (not reached)
+};
+
+struct XentAddArgs {
+    int64_t M, N;
+    uint32_t tiles_n, splits;
+    const float* partials;
+    const float* factor;  // null: 1
+    const float* R;       // the pieces before, or null
+    int64_t ldr;
+    void* C;
+    int64_t ldc;
+};
+
+// C = factor (sum of the splits' partial tiles, in order, + R): a lane takes
+// four values, a workgroup 16 rows of a tile's 256 columns
+template <int O>
+__global__ __launch_bounds__(256) void xent_add_partials(XentAddArgs p)
+{
+    const uint32_t lane = threadIdx.x & 63u, wn = threadIdx.x >> 6, i = blockIdx.x % 8u, wm = blockIdx.x / 8u % 2u, tile = blockIdx.x / 16u;
+    const int64_t row = (int64_t)(tile / p.tiles_n) * 256 + wm * 128 + i * 16 + lane % 16u;
+    const int64_t col0 = (int64_t)(tile % p.tiles_n) * 256 + wn * 64 + 4 * (lane / 16u);
+    if (row >= p.M)
+        return;
+    const float f = p.factor != nullptr ? *p.factor : 1.0f;
+    const float* const share = p.partials + ((size_t)tile * p.splits * 8 + wm * 4 + wn) * 8192 + (i * 4 * 64 + lane) * 4;
+    f32x4 sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sum[j] = *(const f32x4*)(share + j * 256);
+    for (uint32_t s = 1; s < p.splits; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sum[j] += *(const f32x4*)(share + (size_t)s * 65536 + j * 256);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t col = col0 + 16 * j, left = p.N - col;
+        if (left <= 0)
+            continue;
+        const int n = left < 4 ? (int)left : 4;
+        if (p.R != nullptr) {
+            const u32x4 r = load_piece<O_F32>(p.R, row * p.ldr + col, n, n == 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[j][e] += piece_value<O_F32>(r, e);
+        }
+        sum[j] *= f;
+        if constexpr (O == O_F32) {
+            store_piece<O_F32>(p.C, row * p.ldc + col, bit_cast<u32x4>(sum[j]), n, n == 4);
+        } else if (n == 4) {
+            *(u32x2*)((uint16_t*)p.C + row * p.ldc + col) = u32x2{pack2<O>(sum[j][0], sum[j][1]), pack2<O>(sum[j][2], sum[j][3])};
+        } else {
+            for (int e = 0; e < n; ++e)
+                store_value<O>(p.C, row * p.ldc + col + e, sum[j][e]);
+        }
+    }
+}
 
 // --------------------------------------------------------- gradient's rows
 struct XentRowsArgs {
@@ -605,8 +669,36 @@ inline int64_t xent_even(int64_t V, int64_t most)
     return up((V + pieces - 1) / pieces, 256);
 }
 
-// partial tiles of any split plan: one round of 256 x 256 fp32
-constexpr int64_t kXentSplitBytes = (int64_t)64 << 20;
+// Splits of dX's product (K columns of the vocabulary) over workgroups that
+// keep their partial tiles, or 1: the other plans.  In cycles of a compute unit,
+// a step of the 256 tile takes about 2450, a round of workgroups 12000 besides,
+// and adding the partial tiles 10000 and their way out and back at 2500 bytes a
+// cycle.  Up to 128 rows half the tile is idle, and below 4096 tile steps the
+// second launch costs more than the split saves.  Gradients of x alone, M x V x D
+// bf16, us, other plans -> split: 777 x 32003 x 1032 188 -> 152, 2048 x 50000 x
+// 2048 825 -> 705, 512 x 100000 x 4096 868 -> 735, 4096 x 32000 x 1024 564 -> 491,
+// 300 x 100000 x 768 203 -> 191; but 128 x 100000 x 4096 392 -> 408, 100 x 32000 x
+// 1024 42 -> 59, 700 x 10000 x 256 30 -> 42, 4000 x 5000 x 512 68 -> 75.
+inline int64_t xent_dx_splits(int64_t M, int64_t D, int64_t K)
+{
+    const int64_t tiles = n_tiles<256, 256>(M, D), steps = (K + 63) / 64;
+    int64_t best_s = 1;
+    double best = 0.0;
+    if (M <= 128 || tiles * steps < 4096)
+        return 1;
+    for (int64_t s = 1; tiles * s <= 512 && steps / s >= 8; ++s) {
+        const double rounds = (double)((tiles * s + 255) / 256);
+        const double cost = rounds * ((double)steps / s * 2450.0 + 12000.0) + (s > 1 ? 10000.0 + (double)s * M * D * 8.0 / 2500.0 : 0.0);
+        if (best == 0.0 || cost < best) {
+            best = cost;
+            best_s = s;
+        }
+    }
+    return best_s;
+}
+
+// partial tiles of any split plan: two rounds of 256 x 256 fp32
+constexpr int64_t kXentSplitBytes = (int64_t)128 << 20;
 
 struct XentBwd {
     int64_t piece, pieces, ldz;
@@ -679,6 +771,26 @@ tg_status xent_product(const TileArgs& t, const float* factor, const float* R, i
     a.R = R;
     a.ldr = ldr;
     return launch_nt_plan<E, O, B_NCONTIG, EPI_OWN, AL>(a, plan_nt<E, B_NCONTIG>(a.M, a.N, a.K, true), ws, s);
+}
+
+template <int E, int O>
+tg_status xent_dx(const TileArgs& t, const float* factor, const float* R, int64_t ldr, void* ws, hipStream_t s)
+{
+    const int64_t splits = xent_dx_splits(t.M, t.N, t.K);
+    if (splits == 1)
+        return xent_product<E, O, A_KCONTIG>(t, factor, R, ldr, ws, s);
+    XentPartArgs a{};
+    static_cast<TileArgs&>(a) = t;
+    a.group_m = 4;
+    a.splits = (uint32_t)splits;
+    a.partials = (float*)((uint8_t*)ws + kSplitCounterBytes);
+    const tg_status st = launch_nt<E, O_F32, 256, 256, B_NCONTIG, 5, EPI_OWN, A_KCONTIG>(a, (int)splits, s);
+    if (st != TG_OK)
+        return st;
+    const uint32_t tiles_n = (uint32_t)((t.N + 255) / 256);
+    const XentAddArgs p{t.M, t.N, tiles_n, (uint32_t)splits, a.partials, factor, R, ldr, t.C, t.ldc};
+    hipLaunchKernelGGL(xent_add_partials<O>, dim3((uint32_t)(n_tiles<256, 256>(t.M, t.N) * 16)), dim3(256), 0, s, p);
+    return launched();
 }
 
 // (defined in the translation units of their kernels)

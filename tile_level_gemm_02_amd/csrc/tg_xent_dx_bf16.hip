@@ -6,7 +6,7 @@ template <>
 tg_status xent_xgrad<E_BF16>(const TileArgs& t, bool last, const float* factor, const float* R, int64_t ldr, void* ws, hipStream_t s)
 {
     if (last)
-        return xent_product<E_BF16, OutOf<E_BF16>::O, A_KCONTIG>(t, factor, R, ldr, ws, s);
-    return xent_product<E_BF16, O_F32, A_KCONTIG>(t, factor, R, ldr, ws, s);
+        return xent_dx<E_BF16, OutOf<E_BF16>::O>(t, factor, R, ldr, ws, s);
+    return xent_dx<E_BF16, O_F32>(t, factor, R, ldr, ws, s);
 }
 }  // namespace tg
