@@ -39,14 +39,18 @@ struct XentOut {
     float* picked;   // [M]: t of the target
 };
 
-// One value per lane reduced over the lanes that hold the same row (RBK apart)
+// One value per lane reduced over the lanes that hold the same row (RBK apart:
+// the other rows of 16 lanes, the other half of the wave)
 template <int RBK, class F>
 __device__ __forceinline__ float over_row_lanes(float v, F f)
 {
-#pragma unroll
-    for (int d = RBK; d < 64; d *= 2)
-        v = f(v, __shfl_xor(v, d, 64));
-    return v;
+    static_assert(RBK == 16 || RBK == 32, "rows of a matrix instruction");
+    if constexpr (RBK == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(bit_cast<uint32_t>(v), bit_cast<uint32_t>(v), false, false);
+        v = f(bit_cast<float>((uint32_t)r[0]), bit_cast<float>((uint32_t)r[1]));
+    }
+    const auto h = __builtin_amdgcn_permlane32_swap(bit_cast<uint32_t>(v), bit_cast<uint32_t>(v), false, false);
+    return f(bit_cast<float>((uint32_t)h[0]), bit_cast<float>((uint32_t)h[1]));
 }
 
 __device__ __forceinline__ float max2(float a, float b) { return __builtin_fmaxf(a, b); }
@@ -68,9 +72,27 @@ struct XentFwdArgs : TileArgs {
         const int64_t slot = col0 / kXentCols;
         const int left = N - col0 < WC ? (int)(N - col0) : WC;
         const int lg = (int)(lane / RBK);
-        auto rows = [&](auto whole) __attribute__((always_inline)) {
+        constexpr int NB = WR / RBK;
+        // this row's target among the wave's columns, if it is there (the loads
+        // of all rows ahead of their use)
+        int at[NB];
+        int64_t target[NB];
 #pragma unroll
-            for (int i = 0; i < WR / RBK; ++i) {
+        for (int i = 0; i < NB; ++i) {
+            const int64_t row = row0 + i * RBK + lane % RBK;
+            target[i] = row < M ? x.target[row] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t k = target[i] - col0;
+            at[i] = k >= 0 && k < left ? (int)k : -1;
+        }
+        // WHOLE: all columns are there and c is not negative, so that the largest
+        // product is the one with the largest t
+        auto rows = [&](auto whole) __attribute__((always_inline)) {
+            constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
                 const int64_t row = row0 + i * RBK + lane % RBK;
                 float v[NQ * 4], top = -INFINITY;
 #pragma unroll
@@ -78,37 +100,37 @@ struct XentFwdArgs : TileArgs {
                     const f32x4 a = get(i, q);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        v[4 * q + e] = a[e] * x.c;
-                        if (!decltype(whole)::value && q * 4 * G + 4 * lg + e >= left)
+                        v[4 * q + e] = WHOLE ? a[e] : a[e] * x.c;
+                        if (!WHOLE && q * 4 * G + 4 * lg + e >= left)
                             v[4 * q + e] = -INFINITY;
                         top = max2(top, v[4 * q + e]);
                     }
                 }
                 top = over_row_lanes<RBK>(top, max2);
+                top = WHOLE ? top * x.c : top;
                 const float ref = reference_of(top);
                 float sum = 0.0f;
 #pragma unroll
                 for (int k = 0; k < NQ * 4; ++k)
-                    sum += __builtin_amdgcn_exp2f(v[k] - ref);
+                    sum += __builtin_amdgcn_exp2f(WHOLE ? __builtin_fmaf(v[k], x.c, -ref) : v[k] - ref);
                 sum = over_row_lanes<RBK>(sum, add2);
                 if (row < M) {
                     if (lg == 0)
                         x.part[slot * M + row] = f32x2_t{top, sum};
-                    const int64_t at = x.target[row] - col0;
-                    if (at >= 0 && at < left && (int)(at / 4) % G == lg) {
+                    if (at[i] >= 0 && at[i] / 4 % G == lg) {
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
                             const f32x4 a = get(i, q);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if ((int)at == q * 4 * G + 4 * lg + e)
+                                if (at[i] == q * 4 * G + 4 * lg + e)
                                     x.picked[row] = a[e] * x.scale;
                         }
                     }
                 }
             }
         };
-        if (left == WC)
+        if (left == WC && x.c >= 0.0f)
             rows(std::true_type{});
         else
             rows(std::false_type{});
@@ -296,30 +318,47 @@ struct XentGradArgs : TileArgs {
         const int lg4 = 4 * (int)(lane / RBK);
         const int left = N - col0 < WC ? (int)(N - col0) : WC;
         XentRow r[NB];
-        int at[NB];
+        int at[NB], here = 0;
+        bool none[NB];  // (NaN is not equal to 0)
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int64_t row = row0 + i * RBK + lane % RBK;
             r[i] = XentRow{0.0f, 0.0f, 0.0f, -1};
             if (row < M)
                 r[i] = rows[row];
-            const int64_t k = (int64_t)r[i].target - v0 - col0;
-            at[i] = k >= 0 && k < WC ? (int)k : -1;
         }
-        store_rows16<O, RBK, WR, WC>(ep, lane, row0, col0, M, padded, C, ldc, 0, true,
-                                     [&](int i, int q) __attribute__((always_inline)) {
-            const f32x4 v = get(i, q);
-            f32x4 d;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = q * 4 * G + lg4 + e;
-                d[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], c, -r[i].lse2)) * r[i].a;
-                d[e] = col == at[i] ? d[e] - r[i].b : d[e];
-                // (an ignored row is zero whatever its logits; NaN is not equal to 0)
-                d[e] = (r[i].a == 0.0f && r[i].b == 0.0f) || col >= left ? 0.0f : d[e];
-            }
-            return d;
-        });
+        for (int i = 0; i < NB; ++i) {
+            const int64_t k = (int64_t)r[i].target - v0 - col0;
+            at[i] = k >= 0 && k < left ? (int)k : -1;
+            here |= at[i] >= 0;
+            none[i] = r[i].a == 0.0f && r[i].b == 0.0f;
+        }
+        // most tiles hold no row's target (64 columns of a vocabulary), and most
+        // are whole: those run a multiply-add, an exponential, a product and a
+        // selection a value (an ignored row's dt is zero whatever its logits)
+        auto store = [&](auto plain) __attribute__((always_inline)) {
+            store_rows16<O, RBK, WR, WC>(ep, lane, row0, col0, M, padded, C, ldc, 0, true,
+                                         [&](int i, int q) __attribute__((always_inline)) {
+                const f32x4 v = get(i, q);
+                f32x4 d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], c, -r[i].lse2)) * r[i].a;
+                    d[e] = none[i] ? 0.0f : d[e];
+                    if constexpr (!decltype(plain)::value) {
+                        const int col = q * 4 * G + lg4 + e;
+                        d[e] = col == at[i] ? d[e] - r[i].b : d[e];  // (never of an ignored row: it has no target)
+                        d[e] = col >= left ? 0.0f : d[e];
+                    }
+                }
+                return d;
+            });
+        };
+        if (left == WC && __builtin_amdgcn_ballot_w64(here != 0) == 0)
+            store(std::true_type{});
+        else
+            store(std::false_type{});
     }
 };
 
