@@ -113,6 +113,20 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
     const uint32_t vb0 = NB ? krow_off(0u, ldbb, N - n0) : (brow + lrow8) * ldbb + kchunk(0u) * 16u;
     const uint32_t vb1 = NB ? krow_off(1u, ldbb, N - n0) : (brow + lrow8) * ldbb + kchunk(1u) * 16u;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + wave * 4096u;
+    // LEAN (see step_lean): an offset per copy instruction of a K-contiguous
+    // half-stage, out of range where the row is past the last one
+    constexpr bool LEAN = EPI == EPI_OWN;
+    uint32_t oa[4], ob[4];
+    if constexpr (LEAN) {
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+            const uint32_t r = 8u * q + lrow8;
+            oa[q] = (arow + r) * ldab + kchunk(q & 1u) * 16u;
+            oa[q] |= (int32_t)(arow + r) < rows_a ? 0u : kOutOfRange;
+            ob[q] = (brow + r) * ldbb + kchunk(q & 1u) * 16u;
+            ob[q] |= (int32_t)(brow + r) < rows_b ? 0u : kOutOfRange;
+        }
+    }
     // offsets of a half-stage's even and odd copies; a step past the last one
     // and, on edge tiles, chunks past K read out of range (zeros)
     auto half_offs = [&](auto edge, int64_t h, uint32_t& o0, uint32_t& o1) __attribute__((always_inline)) {
@@ -159,6 +173,30 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
         if constexpr (decltype(edge)::value)
             v |= (int32_t)((b ? brow : arow) + 8u * (uint32_t)q + lrow8) < (b ? rows_b : rows_a) ? 0u : kOutOfRange;
         load_lds_1k_at(b ? rb : ra, dst, v, (uint32_t)kt * RB + 8u * (uint32_t)q * (b ? ldbb : ldab));
+    };
+
+    // copy instruction q of half-stage h; `tail`: its step may be past the last
+    // one or hold the end of K
+    auto copy_lean = [&](auto tail, int64_t h, int q, auto src) __attribute__((always_inline)) {
+        const int64_t kt = kt0 + (h >> 1);
+        const bool b = h & 1;
+        const uint32_t dst = lds0 + slot_of(h) + (uint32_t)q * 1024u;
+        const uint32_t past = decltype(tail)::value && (h >> 1) >= NK ? kOutOfRange : 0u;
+        if (b ? NB : NA) {
+            const uint32_t kr = wave * 8u + 2u * (uint32_t)q;
+            uint32_t v = b ? ((q & 1) ? vb1 : vb0) : ((q & 1) ? va1 : va0);
+            if constexpr (decltype(tail)::value)
+                v |= past | (kt * KE + kr + lrow2 < K ? 0u : kOutOfRange);
+            if constexpr (NA)
+                load_lds_1k_at(src, dst, v, kr * (b ? ldbb : ldab));
+            else
+                load_lds_1k_at(rb, dst, v, ((uint32_t)kt * KE + kr) * ldbb);
+            return;
+        }
+        uint32_t v = b ? ob[q] : oa[q];
+        if constexpr (decltype(tail)::value)
+            v |= past | ((int64_t)(kchunk(q & 1) * CE) < K - kt * KE ? 0u : kOutOfRange);
+        load_lds_1k_at(b ? rb : ra, dst, v, (uint32_t)kt * RB);
     };
 
     // ---- fragments of 16 rows and 32 k: lane l holds row l % 16, k range
@@ -292,6 +330,77 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
              },
              n4c, [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH, q, r0, r1, rsrc); });
     };
+    // As step, for kernels with an epilogue of their own.  The step as it is
+    // checks its copies' rows against the tile's on edge tiles, in every tile
+    // where K ends inside a step, all along the loop: 48 us a round of 256 fp16
+    // tiles at K = 1544 where whole steps take 41.  Here the rows' checks are in
+    // the offsets (8 registers, where the base and the row's distance took 4), and
+    // a loop without any runs until the copies reach the end of K.
+    auto step_lean = [&](auto tail, int64_t kt) __attribute__((always_inline)) {
+        const auto psrc = half_src(2 * kt + NH - 1), rsrc = half_src(2 * kt + NH);
+        constexpr bool SPREAD = NH % 2 == 1;
+        auto early = [&](int q0) __attribute__((always_inline)) {
+            return [&, q0](int q) __attribute__((always_inline)) { copy_lean(tail, 2 * kt + NH - 1, q0 + q, psrc); };
+        };
+        unit(0, 0, n6c,
+             [&](int r) __attribute__((always_inline)) {
+                 if (r < 4)
+                     read_a(kt, 0, 1, r);
+                 else
+                     read_b(kt, 1, r - 4);
+             },
+             std::integral_constant<int, SPREAD ? 1 : 4>{}, early(0));
+        unit(1, 0, n6c,
+             [&](int r) __attribute__((always_inline)) {
+                 if (r == 0)
+                     read_a(kt, 1, 0, 0);
+                 else if (r < 3)
+                     read_b(kt, 1, r + 1);
+                 else
+                     read_a(kt, 1, 0, r - 2);
+             },
+             std::integral_constant<int, SPREAD ? 1 : 0>{}, early(1));
+        unit(0, 1, n4c, [&](int r) __attribute__((always_inline)) { read_a(kt, 1, 1, r); },
+             std::integral_constant<int, SPREAD ? 2 : 0>{}, early(2));
+        __builtin_amdgcn_sched_barrier(0);
+        wait_copies<4 * (NH - 4)>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        unit(1, 1, n8c,
+             [&](int r) __attribute__((always_inline)) {
+                 if (r == 0)
+                     read_a(kt + 1, 0, 0, 0);
+                 else if (r < 5)
+                     read_b(kt + 1, 0, r - 1);
+                 else
+                     read_a(kt + 1, 0, 0, r - 4);
+             },
+             n4c, [&](int q) __attribute__((always_inline)) { copy_lean(tail, 2 * kt + NH, q, rsrc); });
+    };
+    auto run_lean = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < NH - 1; ++h) {
+            const auto src = half_src(h);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                copy_lean(std::true_type{}, h, q, src);
+        }
+        wait_copies<4 * (NH - 3)>();  // step 0 landed
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            read_a(0, 0, 0, r);
+            read_b(0, 0, r);
+        }
+        // step kt copies for steps up to kt + 2
+        const int64_t inside = K / KE - kt0, whole = (inside < NK ? inside : NK) - 2;
+        int64_t kt = 0;
+        for (; kt < whole; ++kt)
+            step_lean(std::false_type{}, kt);
+        for (; kt < NK; ++kt)
+            step_lean(std::true_type{}, kt);
+        wait_copies<0>();
+    };
     auto run = [&](auto edge) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < NH - 1; ++h) {
@@ -314,8 +423,9 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
         wait_copies<0>();  // copies past the last step (zeros) must land before LDS is reused
     };
     if (NK > 0) {
-        const bool tail = K % KE != 0 && (!std::is_base_of<KeepsPartials, P>::value || kt0 + NK == KT);
-        if (rows_a == BM && rows_b == BNO && !tail)  // full tiles, no K tail
+        if constexpr (LEAN)
+            run_lean();
+        else if (rows_a == BM && rows_b == BNO && K % KE == 0)  // full tiles, no K tail
             run(std::false_type{});
         else
             run(std::true_type{});
