@@ -257,3 +257,37 @@ def test_a_tensor_past_32_bit_offsets(tg):
         else:
             assert abs(float(m[-1]) + 0.1) < 1e-7 and abs(float(v[n // 2]) - 0.05 * 0.0625) < 1e-8
         del p, g, m, v
+
+
+def test_wrong_tensors_are_refused(tg):
+    z = lambda n, dtype=F32: torch.zeros(n, device="cuda", dtype=dtype)  # noqa: E731
+    p, f8, s = z(300), z(300, torch.uint8).view(F8), z(2)
+
+    def no(match, *a, **k):
+        with pytest.raises(ValueError, match=match):
+            tg.tg_adamw(*a, **({"step": 1, "lr": 1e-3} | k))
+
+    no("for each parameter", [p], [], [p], [p])
+    no("for each parameter", [], [p], [], [])
+    no("for each parameter", [p], [p], [p], [p], masters=[])
+    no("come together", [p], [p], [f8], [f8], exp_avg_scales=[s])
+    no("float32, float16 or bfloat16", [p.double()], [p], [p], [p])
+    no("exp_avg must be float32", [p], [p], [p.half()], [p])
+    no("exp_avg must be float8", [p], [p], [p], [p], exp_avg_scales=[s], exp_avg_sq_scales=[s])
+    no("exp_avg must be float32", [p], [p], [f8], [f8])
+    no("grads must match", [p], [z(299)], [p], [p])
+    no("exp_avg_scales must match", [p], [p], [f8], [f8], exp_avg_scales=[z(1)], exp_avg_sq_scales=[s])
+    no("masters go with", [p], [p], [p], [p], masters=[p])
+    no("contiguous", [z(600)[::2]], [p], [p], [p])
+    no("not", [p], [p.cpu()], [p], [p])
+    no("norm", [p], [p], [p], [p], norm=s)
+    no("step", [p], [p], [p], [p], step=z(1))
+    no("lr", [p], [p], [p], [p], lr=z(1, torch.float64))
+    with pytest.raises(TypeError):
+        tg.tg_adamw([p], [p], [p], [p], 1.5, 1e-3)
+    with pytest.raises(tg.TGError):
+        tg.tg_adamw([p], [p], [p], [p], 0, 1e-3)
+    q, g, m, v = (z(300) for _ in range(4))
+    tg.tg_adamw((q,), (g + 1,), iter([m]), [v], 1, 1e-3, weight_decay=0.0)  # any sequences
+    assert abs(float(q[7]) + 1e-3) < 1e-8
+    tg.tg_adamw([], [], [], [], 1, 1e-3)

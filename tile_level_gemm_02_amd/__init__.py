@@ -23,7 +23,9 @@ Entry points (same names as the C ABI):
     tg_status_string(code), tg_version()
 
 The feed-forward operators of include/tg_ops.h (tg_linear, tg_glu, their
-gradients, tg_clip_grads) are bound in ``ops.py`` and exported here too.
+gradients, tg_clip_grads) are bound in ``ops.py``, the vocabulary loss and the
+AdamW step of include/tg_train.h in ``train.py``, and the 8-bit integer layers
+of include/tg_int8.h in ``int8.py``; all are exported here too.
 
 Tensor conventions: A is M x K; for b_layout "row" B is the K x N matrix, for
 "col" B is its N x K storage (the transpose_B / nn.Linear layout); C is M x N

@@ -1,12 +1,13 @@
 """Build libtg.so (the HIP kernels + C ABI) in-tree with hipcc for gfx950, and
-the native helper of the tg_clip_grads binding, _tgbind.so, with g++.
+the binding's native helper, _tgbind.so, with g++.
 
     python -m tile_level_gemm_02_amd.build          # or build() from Python
 
 Each csrc/*.hip file is compiled to an object under _build/ (in parallel),
 then linked into tile_level_gemm_02_amd/libtg.so.  The library needs neither
 g++ nor torch's C++ headers; where the helper cannot be built, build() says so
-in a warning and only the Python tg_clip_grads is missing.
+in a warning and only the Python calls that need it are missing (tg_clip_grads,
+tg_adamw, the int8 layers).
 """
 from __future__ import annotations
 
@@ -88,7 +89,7 @@ def build(extra: list[str] | None = None, jobs: int | None = None) -> str:
     except Exception as e:  # no g++, no headers, or ones that bind.cpp does not fit
         if os.path.exists(BIND):
             os.remove(BIND)  # (of other sources or headers)
-        warnings.warn(f"{BIND} was not built, tg_clip_grads cannot be called from Python: {e}", RuntimeWarning, stacklevel=2)
+        warnings.warn(f"{BIND} was not built, tg_clip_grads, tg_adamw and the int8 layers cannot be called from Python: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 

@@ -182,15 +182,17 @@ PyObject* adamw(PyObject*, PyObject* args)
                 return nullptr;
         } else {
             step = PyLong_AsLongLong(step_o);
+            if (step == -1 && PyErr_Occurred())
+                return nullptr;
         }
         if (THPVariable_Check(lr_o)) {
             if ((pl = scalar_on(lr_o, dev, at::kFloat, "lr")) == nullptr)
                 return nullptr;
         } else {
             lr = PyFloat_AsDouble(lr_o);
+            if (lr == -1.0 && PyErr_Occurred())
+                return nullptr;
         }
-        if (PyErr_Occurred())
-            return nullptr;
         const tg_status st = ((adamw_fn)(uintptr_t)fn)(n, t.data(), step, lr, beta1, beta2, eps, decay, (const float*)pn, max_norm,
                                                        (const int64_t*)ps, (const float*)pl, (void*)(uintptr_t)stream);
         return PyLong_FromLong((long)st);

@@ -42,10 +42,10 @@ _BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tgbind.s
 
 
 def _load_bind():
-    """The helper, loaded by the first tg_clip_grads: the products do without it."""
+    """The helper, loaded by the first call that needs it (tg_clip_grads, tg_adamw, the int8 layers): the other products do without."""
     global _bind, _clip_address
     if not os.path.exists(_BIND_PATH):
-        raise ImportError(f"{_BIND_PATH}, which tg_clip_grads needs, is not built; run `python -m tile_level_gemm_02_amd.build`")
+        raise ImportError(f"{_BIND_PATH}, which tg_clip_grads, tg_adamw and the int8 layers need, is not built; run `python -m tile_level_gemm_02_amd.build`")
     loader = importlib.machinery.ExtensionFileLoader("_tgbind", _BIND_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tgbind", loader))
     loader.exec_module(module)

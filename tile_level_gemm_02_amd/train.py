@@ -154,18 +154,17 @@ def tg_adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), e
     min(1, max_norm / (norm + 1e-6)); a norm that is not finite leaves
     everything as it is.  ``step`` (1 for the first) and ``lr`` may be tensors
     of one int64 and one float32 on the GPU, for a captured step."""
-    if not params:
+    lists = [v if v is None or type(v) is list else list(v)
+             for v in (params, grads, exp_avg, exp_avg_sq, masters, exp_avg_scales, exp_avg_sq_scales)]
+    if not any(lists):
         return
-    lib = _fns or _lib()
+    if _fns is None:
+        _lib()
     if _ops._bind is None:
         _ops._load_bind()
-    dev = _device(params[0], "params[0]")
-
-    def listed(v):
-        return v if v is None or type(v) is list else list(v)
-
-    code = _ops._bind.adamw(_adamw_address, listed(params), listed(grads), listed(exp_avg), listed(exp_avg_sq), listed(masters),
-                            listed(exp_avg_scales), listed(exp_avg_sq_scales), step, lr, betas[0], betas[1], eps, weight_decay, norm,
-                            max_norm, dev, _current_stream(dev) if stream is None else _stream(stream))
+    first = next(v[0] for v in lists if v)
+    dev = _device(first, "the first tensor")
+    code = _ops._bind.adamw(_adamw_address, *lists, step, lr, betas[0], betas[1], eps, weight_decay, norm, max_norm, dev,
+                            _current_stream(dev) if stream is None else _stream(stream))
     if code:
         raise TGError("tg_adamw", code)
