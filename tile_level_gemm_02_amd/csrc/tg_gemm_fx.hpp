@@ -113,8 +113,14 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
     const uint32_t vb0 = NB ? krow_off(0u, ldbb, N - n0) : (brow + lrow8) * ldbb + kchunk(0u) * 16u;
     const uint32_t vb1 = NB ? krow_off(1u, ldbb, N - n0) : (brow + lrow8) * ldbb + kchunk(1u) * 16u;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + wave * 4096u;
-    // LEAN (see step_lean): an offset per copy instruction of a K-contiguous
-    // half-stage, out of range where the row is past the last one
+    // LEAN (kernels with an epilogue of their own): the copies' row checks are in
+    // an offset per copy instruction of a K-contiguous half-stage, out of range
+    // where the row is past the last one (8 registers; base and distance took 4),
+    // and the loop runs without any check until the copies reach the end of K.
+    // The other kernels compare their copies' rows with the tile's on edge tiles,
+    // in every tile where K ends inside a step, all along the loop: 48 us a round
+    // of 256 fp16 tiles at K = 1544, where this takes 45, and 4% less with none
+    // at all to check (4096 x 128256 x 4096 3118 -> 3004 us).
     constexpr bool LEAN = EPI == EPI_OWN;
     uint32_t oa[4], ob[4];
     if constexpr (LEAN) {
@@ -197,6 +203,13 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
         if constexpr (decltype(tail)::value)
             v |= past | ((int64_t)(kchunk(q & 1) * CE) < K - kt * KE ? 0u : kOutOfRange);
         load_lds_1k_at(b ? rb : ra, dst, v, (uint32_t)kt * RB);
+    };
+
+    auto copy = [&](auto edge, int64_t h, int q, uint32_t o0, uint32_t o1, auto src) __attribute__((always_inline)) {
+        if constexpr (LEAN)
+            copy_lean(edge, h, q, src);
+        else
+            copy_half(edge, h, q, o0, o1, src);
     };
 
     // ---- fragments of 16 rows and 32 k: lane l holds row l % 16, k range
@@ -284,14 +297,17 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
     // holds B rows of step kt+1, needed at this step's barrier, and goes out
     // at once.  8192 x 4096 x 10240 with a residual 578 -> 565 us with five,
     // gated 4096 x 10240 x 4096 532 -> 516 (interleaved, snake order included).
+    // (LEAN: `edge` is copy_lean's `tail`)
     auto step = [&](auto edge, int64_t kt) __attribute__((always_inline)) {
-        uint32_t p0, p1, r0, r1;
-        half_offs(edge, 2 * kt + NH - 1, p0, p1);
-        half_offs(edge, 2 * kt + NH, r0, r1);
+        uint32_t p0 = 0u, p1 = 0u, r0 = 0u, r1 = 0u;
+        if constexpr (!LEAN) {
+            half_offs(edge, 2 * kt + NH - 1, p0, p1);
+            half_offs(edge, 2 * kt + NH, r0, r1);
+        }
         const auto psrc = half_src(2 * kt + NH - 1), rsrc = half_src(2 * kt + NH);
         constexpr bool SPREAD = NH % 2 == 1;
         auto early = [&](int q0) __attribute__((always_inline)) {
-            return [&, q0](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH - 1, q0 + q, p0, p1, psrc); };
+            return [&, q0](int q) __attribute__((always_inline)) { copy(edge, 2 * kt + NH - 1, q0 + q, p0, p1, psrc); };
         };
         unit(0, 0, n6c,
              [&](int r) __attribute__((always_inline)) {
@@ -328,54 +344,7 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
                  else
                      read_a(kt + 1, 0, 0, r - 4);
              },
-             n4c, [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH, q, r0, r1, rsrc); });
-    };
-    // As step, for kernels with an epilogue of their own.  The step as it is
-    // checks its copies' rows against the tile's on edge tiles, in every tile
-    // where K ends inside a step, all along the loop: 48 us a round of 256 fp16
-    // tiles at K = 1544 where whole steps take 41.  Here the rows' checks are in
-    // the offsets (8 registers, where the base and the row's distance took 4), and
-    // a loop without any runs until the copies reach the end of K.
-    auto step_lean = [&](auto tail, int64_t kt) __attribute__((always_inline)) {
-        const auto psrc = half_src(2 * kt + NH - 1), rsrc = half_src(2 * kt + NH);
-        constexpr bool SPREAD = NH % 2 == 1;
-        auto early = [&](int q0) __attribute__((always_inline)) {
-            return [&, q0](int q) __attribute__((always_inline)) { copy_lean(tail, 2 * kt + NH - 1, q0 + q, psrc); };
-        };
-        unit(0, 0, n6c,
-             [&](int r) __attribute__((always_inline)) {
-                 if (r < 4)
-                     read_a(kt, 0, 1, r);
-                 else
-                     read_b(kt, 1, r - 4);
-             },
-             std::integral_constant<int, SPREAD ? 1 : 4>{}, early(0));
-        unit(1, 0, n6c,
-             [&](int r) __attribute__((always_inline)) {
-                 if (r == 0)
-                     read_a(kt, 1, 0, 0);
-                 else if (r < 3)
-                     read_b(kt, 1, r + 1);
-                 else
-                     read_a(kt, 1, 0, r - 2);
-             },
-             std::integral_constant<int, SPREAD ? 1 : 0>{}, early(1));
-        unit(0, 1, n4c, [&](int r) __attribute__((always_inline)) { read_a(kt, 1, 1, r); },
-             std::integral_constant<int, SPREAD ? 2 : 0>{}, early(2));
-        __builtin_amdgcn_sched_barrier(0);
-        wait_copies<4 * (NH - 4)>();
-        __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
-        unit(1, 1, n8c,
-             [&](int r) __attribute__((always_inline)) {
-                 if (r == 0)
-                     read_a(kt + 1, 0, 0, 0);
-                 else if (r < 5)
-                     read_b(kt + 1, 0, r - 1);
-                 else
-                     read_a(kt + 1, 0, 0, r - 4);
-             },
-             n4c, [&](int q) __attribute__((always_inline)) { copy_lean(tail, 2 * kt + NH, q, rsrc); });
+             n4c, [&](int q) __attribute__((always_inline)) { copy(edge, 2 * kt + NH, q, r0, r1, rsrc); });
     };
     auto run_lean = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -396,9 +365,9 @@ __global__ __launch_bounds__(512) void gemm_fx(P p)
         const int64_t inside = K / KE - kt0, whole = (inside < NK ? inside : NK) - 2;
         int64_t kt = 0;
         for (; kt < whole; ++kt)
-            step_lean(std::false_type{}, kt);
+            step(std::false_type{}, kt);
         for (; kt < NK; ++kt)
-            step_lean(std::true_type{}, kt);
+            step(std::true_type{}, kt);
         wait_copies<0>();
     };
     auto run = [&](auto edge) __attribute__((always_inline)) {

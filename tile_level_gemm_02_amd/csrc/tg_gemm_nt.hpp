@@ -416,6 +416,52 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
                        (uint32_t)kt * RB + (uint32_t)(RPI * q) * ((h & 1) ? ldbb : ldab));
     };
 
+    // Kernels with an epilogue of their own: as gemm_fx's LEAN copies
+    constexpr bool LEAN = EPI == EPI_OWN;
+    static_assert(!LEAN || (!GLU && !(NB && EB == 1)), "operands of the kernels with an epilogue of their own");
+    uint32_t oa[AI], ob[BI];
+    if constexpr (LEAN) {
+#pragma unroll
+        for (uint32_t q = 0; q < (uint32_t)AI; ++q) {
+            const uint32_t r = wave * (BM / NW) + RPI * q + lrowi;
+            oa[q] = r * ldab + ((q & 1u) ? lchunk1 : lchunk0) * 16u;
+            oa[q] |= (int32_t)r < rows_a ? 0u : kOutOfRange;
+        }
+#pragma unroll
+        for (uint32_t q = 0; q < (uint32_t)BI; ++q) {
+            const uint32_t r = wave * (BN / NW) + RPI * q + lrowi;
+            ob[q] = r * ldbb + ((q & 1u) ? lchunk1 : lchunk0) * 16u;
+            ob[q] |= (int32_t)r < rows_b ? 0u : kOutOfRange;
+        }
+    }
+    auto copy_lean = [&](auto tail, int64_t h, int q, auto src) __attribute__((always_inline)) {
+        const int64_t kt = kt0 + (h >> 1);
+        const bool b = h & 1;
+        const uint32_t past = decltype(tail)::value && (h >> 1) >= NK ? kOutOfRange : 0u;
+        const uint32_t dst = half_dst(h) + q * 1024;
+        if (b ? NB : NA) {
+            const uint32_t kr = b ? (wave * BI + (uint32_t)q) * RPIN : (wave * AI + (uint32_t)q) * RPIM;
+            uint32_t v = b ? ((q & 1) ? vb1 : vb0) : ((q & 1) ? va1 : va0);
+            if constexpr (decltype(tail)::value)
+                v |= past | (kt * KE + kr + (b ? lrown : lrowm) < K ? 0u : kOutOfRange);
+            if constexpr (NA)
+                load_lds_1k_at(src, dst, v, kr * (b ? ldbb : ldab));
+            else
+                load_lds_1k_at(rb, dst, v, ((uint32_t)kt * KE + kr) * ldbb);
+            return;
+        }
+        uint32_t v = b ? ob[q] : oa[q];
+        if constexpr (decltype(tail)::value)
+            v |= past | ((int64_t)(((q & 1) ? lchunk1 : lchunk0) * CE) < K - kt * KE ? 0u : kOutOfRange);
+        load_lds_1k_at(b ? rb : ra, dst, v, (uint32_t)kt * RB);
+    };
+    auto copy = [&](auto edge, int64_t h, int q, uint32_t o0, uint32_t o1, auto src) __attribute__((always_inline)) {
+        if constexpr (LEAN)
+            copy_lean(edge, h, q, src);
+        else
+            copy_half(edge, h, q, o0, o1, src);
+    };
+
     // ---- fragment reads: every fragment row of this lane has the same swz(row)
     const uint32_t wm = wave / WN, wn = wave % WN;
     const uint32_t lrow = lane & 31u, lgrp = lane >> 5;
@@ -567,10 +613,13 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
     // publishes step kt+1 (half-stages past 2kt+3 may still be in flight) and
     // frees the two half-stages of step kt: half-stage 2kt+NH is copied during
     // the last sub-step, while the first fragments of step kt+1 are read.
+    // (LEAN: `edge` is copy_lean's `tail`)
     auto step = [&](auto edge, int64_t kt) __attribute__((always_inline)) {
-        uint32_t p0, p1, r0, r1;
-        half_offs(edge, 2 * kt + NH - 1, p0, p1);
-        half_offs(edge, 2 * kt + NH, r0, r1);
+        uint32_t p0 = 0u, p1 = 0u, r0 = 0u, r1 = 0u;
+        if constexpr (!LEAN) {
+            half_offs(edge, 2 * kt + NH - 1, p0, p1);
+            half_offs(edge, 2 * kt + NH, r0, r1);
+        }
         const auto psrc = half_src(2 * kt + NH - 1), rsrc = half_src(2 * kt + NH);
 #pragma unroll
         for (int s = 0; s < KSTEPS - 1; ++s) {
@@ -580,7 +629,7 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
             // half-stage, during the second: 1-4% faster at 3072^3 .. 3584^3)
             if (s == ((NH & 1) && KSTEPS > 2 ? 1 : 0))
                 substep(s & 1, rd,
-                        [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH - 1, q, p0, p1, psrc); },
+                        [&](int q) __attribute__((always_inline)) { copy(edge, 2 * kt + NH - 1, q, p0, p1, psrc); },
                         std::integral_constant<int, ((NH - 1) & 1) ? BI : AI>{});
             else
                 substep(s & 1, rd, nothing, std::integral_constant<int, 0>{});
@@ -591,7 +640,7 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
         __builtin_amdgcn_sched_barrier(0);
         // (the reads of step kt+1 after the last step are stale and unused)
         substep((KSTEPS - 1) & 1, [&](int r) __attribute__((always_inline)) { read_frag(kt + 1, 0, 0, r); },
-                [&](int q) __attribute__((always_inline)) { copy_half(edge, 2 * kt + NH, q, r0, r1, rsrc); },
+                [&](int q) __attribute__((always_inline)) { copy(edge, 2 * kt + NH, q, r0, r1, rsrc); },
                 std::integral_constant<int, (NH & 1) ? BI : AI>{});
     };
 
@@ -613,8 +662,30 @@ __device__ __forceinline__ void gemm_nt_body(const P& p, uint32_t bid, uint32_t 
             step(edge, kt);
         wait_copies<0>();  // copies past the last step (zeros) must land before LDS is reused
     };
+    auto run_lean = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < NH - 1; ++h) {
+            const auto src = half_src(h);
+#pragma unroll
+            for (int j = 0; j < ((h & 1) ? BI : AI); ++j)
+                copy_lean(std::true_type{}, h, j, src);
+        }
+        wait_copies<copies_in(2, NH - 1)>();  // step 0 landed
+        __syncthreads();
+        read_frags(0, 0, 0);
+        // step kt copies for steps up to kt + NH / 2
+        const int64_t inside = K / KE - kt0, whole = (inside < NK ? inside : NK) - NH / 2;
+        int64_t kt = 0;
+        for (; kt < whole; ++kt)
+            step(std::false_type{}, kt);
+        for (; kt < NK; ++kt)
+            step(std::true_type{}, kt);
+        wait_copies<0>();
+    };
     if (NK > 0) {
-        if (rows_a == BM && rows_b == BNO && K % KE == 0)  // full tiles, no K tail
+        if constexpr (LEAN)
+            run_lean();
+        else if (rows_a == BM && rows_b == BNO && K % KE == 0)  // full tiles, no K tail
             run(std::false_type{});
         else
             run(std::true_type{});
