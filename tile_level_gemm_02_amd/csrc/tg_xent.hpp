@@ -478,59 +478,67 @@ struct XentRowsArgs {
     int64_t ignore;
     float z, scale, grad_scale, lift;  // lift: 2^12 for fp16, 1 for bf16
     const float *lse, *dloss, *total;
+    const float* most;  // the largest row factor (xent_most), or null: 1
     XentRow* rows;
     float* factor;
 };
 
-// One workgroup: the largest factor of a row that counts, as a power of two at
-// or above it, and each row's numbers relative to it.  What it divides out (and
-// `lift`) returns in the products' factor.
+// The largest factor of a row that counts, by one workgroup
 template <int = 0>
-__global__ __launch_bounds__(1024) void xent_rows(XentRowsArgs p)
+__global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
 {
     __shared__ float red[16];
     const uint32_t tid = threadIdx.x;
-    float most = 1.0f;
-    if (p.dloss != nullptr || p.z != 0.0f) {
-        most = 0.0f;
-        for (int64_t i = tid; i < p.M; i += 1024)
-            if (p.target[i] != p.ignore) {
-                const float b = p.dloss != nullptr ? __builtin_fabsf(p.dloss[i]) : 1.0f;
-                most = max2(most, max2(b, b * __builtin_fabsf(1.0f + 2.0f * p.z * p.lse[i])));
-            }
+    float most = 0.0f;
+    for (int64_t i = tid; i < p.M; i += 1024)
+        if (p.target[i] != p.ignore) {
+            const float b = p.dloss != nullptr ? __builtin_fabsf(p.dloss[i]) : 1.0f;
+            most = max2(most, max2(b, b * __builtin_fabsf(1.0f + 2.0f * p.z * p.lse[i])));
+        }
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1)
-            most = max2(most, __shfl_xor(most, d, 64));
-        if ((tid & 63u) == 0u)
-            red[tid >> 6] = most;
-        __syncthreads();
-        for (int k = 0; k < 16; ++k)
-            most = max2(most, red[k]);
-    }
+    for (int d = 32; d > 0; d >>= 1)
+        most = max2(most, __shfl_xor(most, d, 64));
+    if ((tid & 63u) == 0u)
+        red[tid >> 6] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        most = max2(most, red[k]);
+    if (tid == 0u)
+        *out = most;
+}
+
+// Each row's numbers relative to a power of two at or above the largest; what
+// that (and `lift`) divides out returns in the products' factor.
+template <int = 0>
+__global__ __launch_bounds__(256) void xent_rows(XentRowsArgs p)
+{
     // 2^e >= most, within fp32's normal numbers (infinity, and none at all: 1)
     int e = 0;
-    if (most > 0.0f && most < INFINITY) {
+    const float most = p.most != nullptr ? *p.most : 1.0f;
+    if (most > 0.0f && most < INFINITY && most != 1.0f) {
         (void)frexpf(most, &e);
         e = e < -100 ? -100 : e;
     }
     const float down = ldexpf(1.0f, -e) * p.lift;  // (e <= 128, lift <= 2^12: a normal number or a subnormal 2^-128)
-    for (int64_t i = tid; i < p.M; i += 1024) {
-        const int64_t t = p.target[i];
-        XentRow r{0.0f, 0.0f, 0.0f, -1};
-        if (t != p.ignore) {
-            const bool known = t >= 0 && t < p.V;
-            const float lse = p.lse[i];
-            r.lse2 = lse * 1.44269504088896341f;
-            r.b = known ? (p.dloss != nullptr ? p.dloss[i] * down : down) : NAN;
-            r.a = r.b * (1.0f + 2.0f * p.z * lse);
-            r.target = known ? (int32_t)t : -1;
-        }
-        p.rows[i] = r;
-    }
-    if (tid == 0u) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i == 0) {
         const float count = p.total != nullptr ? max2(p.total[1], 1.0f) : 1.0f;
         *p.factor = (float)((double)p.scale * (double)p.grad_scale * ldexp(1.0, e) / ((double)p.lift * (double)count));
     }
+    if (i >= p.M)
+        return;
+    const int64_t t = p.target[i];
+    XentRow r{0.0f, 0.0f, 0.0f, -1};
+    if (t != p.ignore) {
+        const bool known = t >= 0 && t < p.V;
+        const float lse = p.lse[i];
+        r.lse2 = lse * 1.44269504088896341f;
+        r.b = known ? (p.dloss != nullptr ? p.dloss[i] * down : down) : NAN;
+        r.a = r.b * (1.0f + 2.0f * p.z * lse);
+        r.target = known ? (int32_t)t : -1;
+    }
+    p.rows[i] = r;
 }
 
 // --------------------------------------------------------------- host side
@@ -683,14 +691,17 @@ tg_status xent_forward(const XentCall& q)
     return launched();
 }
 
-// Columns of a piece: dt takes at most kXentPieceBytes, and a piece's rows of
-// W lie within one buffer descriptor (as nt_eligible_nrow asks).
-constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
+// Columns of a piece: as many as dt holds in kXentPieceBytes, kXentPiece with
+// many rows (each piece reads and writes dX's fp32 sums), and a piece's rows of
+// W lie within one buffer descriptor (as nt_eligible_nrow asks).  From 256 MiB to
+// 1 GiB the gradients take the same time within 1% (4096 x 128256 x 4096; 4% at
+// 8192 x 131072 x 1024), 128 MiB costs 1 to 13% and 64 MiB 2 to 30.
+constexpr int64_t kXentPieceBytes = (int64_t)512 << 20, kXentPiece = 8192;
 
 inline int64_t xent_most_piece(int64_t M, int64_t V, int64_t ldw)
 {
     int64_t most = kXentPieceBytes / (2 * (M < 1 ? 1 : M)) / 256 * 256;
-    most = most < 256 ? 256 : most;
+    most = most < kXentPiece ? kXentPiece : most;
     const int64_t fits = ((int64_t)kNumRecords - 1024) / (2 * (ldw < 1 ? 1 : ldw)) - 512;
     if (most > 131072)
         most = 131072;
@@ -854,8 +865,14 @@ tg_status xent_backward(const XentCall& q)
     float* const factor = (float*)(ws + b.factor);
     float* const sums = (float*)(ws + b.sums);
     const int64_t lds = up(q.D, 4);
-    XentRowsArgs r{q.M, q.V, q.target, q.ignore, q.z, q.scale, q.grad_scale, E == E_F16 ? 4096.0f : 1.0f, q.lse, q.dloss, q.total, rows, factor};
-    hipLaunchKernelGGL(xent_rows<>, dim3(1), dim3(1024), 0, q.s, r);
+    XentRowsArgs r{q.M, q.V, q.target, q.ignore, q.z, q.scale, q.grad_scale, E == E_F16 ? 4096.0f : 1.0f, q.lse, q.dloss, q.total, nullptr, rows, factor};
+    // factors of the rows' own are taken relative to the largest; 1 + 2 z lse is
+    // near enough to 1 for bf16's range
+    if (q.dloss != nullptr || (E == E_F16 && q.z != 0.0f)) {
+        hipLaunchKernelGGL(xent_most<>, dim3(1), dim3(1024), 0, q.s, r, factor + 1);
+        r.most = factor + 1;
+    }
+    hipLaunchKernelGGL(xent_rows<>, dim3((uint32_t)((q.M + 255) / 256 + (q.M == 0))), dim3(256), 0, q.s, r);
     tg_status st = launched();
     for (int64_t i = 0; i < b.pieces && st == TG_OK; ++i) {
         const int64_t v0 = i * b.piece, n = q.V - v0 < b.piece ? q.V - v0 : b.piece;
