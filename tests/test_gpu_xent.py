@@ -127,6 +127,8 @@ def backward_case(tg, M, V, D, dtype, dw_dtype, piece=0, weighted=False, counted
 @pytest.mark.parametrize("M,V,D,piece", [(1, 1, 8, 0), (1, 300, 64, 0), (5, 257, 72, 1), (33, 1000, 136, 256), (100, 769, 520, 1),
                                          (300, 5003, 264, 1024), (777, 3201, 136, 0), (1270, 1281, 72, 512), (200, 70003, 64, 0),
                                          (512, 9000, 1032, 4096), (2300, 2290, 136, 0), (4100, 513, 256, 0), (4352, 4400, 64, 0),
+                                         # one piece, which has no sums of dx, needs less than two
+                                         (160, 452, 1256, 512), (160, 452, 1256, 1),
                                          # dx's K, the vocabulary, over workgroups whose partial tiles a kernel adds; over pieces as well
                                          (600, 70003, 264, 0), (600, 70003, 264, 65536), (129, 131080, 520, 0)])
 @pytest.mark.parametrize("dtype,dw_dtype", [(BF, BF), (BF, F32), (F16, F16), (F16, F32)])

@@ -91,7 +91,7 @@ def test_loss_gradient_refusals(tg, train):
 
 def test_loss_workspace_queries(tg):
     bf = torch.bfloat16
-    for M, V, D in ((1, 1, 8), (7, 32000, 2048), (4096, 128256, 4096), (100000, 200000, 1024), (2000000, 1000, 64)):
+    for M, V, D in ((1, 1, 8), (7, 32000, 2048), (160, 452, 1256), (4096, 128256, 4096), (100000, 200000, 1024), (2000000, 1000, 64)):
         n = [tg.tg_linear_xent_backward_workspace_bytes(bf, M, V, D, p) for p in (1, 256, 257, 4096, 0)]
         assert 0 < n[0] == n[1] <= n[2] and n[1] <= n[4] and n[3] <= n[4], (M, V, D, n)
         assert n[4] <= (128 << 20) + (1 << 20) + M * (16 + 4 * D) + max(512 << 20, 2 * 8192 * M), (M, V, D, n)

@@ -792,8 +792,13 @@ inline int64_t xent_bwd_bytes(int64_t M, int64_t V, int64_t D, int64_t ldw, int6
     const int64_t most = xent_most_piece(M, V, ldw);
     if (most < 256)
         return -1;
-    piece = piece == 0 ? xent_even(V, most) : piece > most ? xent_even(V, most) : up(piece, 256);
-    return xent_bwd_layout(M, V, D, piece).bytes;
+    piece = piece == 0 || piece > most ? xent_even(V, most) : up(piece, 256);
+    const int64_t bytes = xent_bwd_layout(M, V, D, piece).bytes;
+    if (up(V, 256) > most)
+        return bytes;
+    // one piece needs no room for dX's sums, and may take less than several
+    const int64_t whole = xent_bwd_layout(M, V, D, up(V, 256)).bytes;
+    return whole < bytes ? whole : bytes;
 }
 
 // dt of a piece
