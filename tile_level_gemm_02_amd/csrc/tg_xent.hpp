@@ -12,7 +12,13 @@
 // vocabulary at a time, the same product again with dt as its epilogue,
 // rounded to 16 bits, then the two products that take dt as their operand.
 // All of them are bound by the matrix products: 2 M V D operations forward
-// and 6 for the gradient.
+// and 6 for the gradient.  Bf16 8192 x 131072 x 4096 6.2 ms forward, 1420
+// TFLOP/s (a library product of the same size, which stores its logits, 1490);
+// gradients of 4096 x 128256 x 4096 9.4 ms, 1370; 7 x 32000 x 2048 27 us, 4.8
+// TB/s of the weight.  The forward epilogue takes 4.5 us a round of 256 tiles,
+// 1.1 of them exponentials.  Smaller tiles (128, 256 x 128) for dt, of which two
+// workgroups or a shorter epilogue would overlap, ran 8 to 50% slower at every
+// size tried.
 //
 // Exponentials are base 2: with c = scale log2(e), e^(t - lse) is
 // exp2(acc c - lse log2(e)), one multiply-add and one instruction per value.
@@ -362,8 +368,8 @@ struct XentGradArgs : TileArgs {
     }
 };
 
-// The products that take dt: C = alpha (acc + R), alpha in device memory, R
-// the fp32 sums over the pieces before (or null).  O_F32 with alpha null
+// The products that take dt: C = factor (acc + R), the factor in device memory,
+// R the fp32 sums over the pieces before (or null).  O_F32 without a factor
 // keeps such sums.
 template <int O>
 struct XentProdArgs : TileArgs {
