@@ -72,6 +72,20 @@ def test_quantized_rows(tg, M, K, dtype):
     assert float(((q.double() * scale[:M, None].double() - x.double()).abs() - 0.5 * scale[:M, None].double() * (1 + 2.0 ** -16)).max()) <= 0.0
 
 
+def test_more_rows_than_a_launch_has_room_for(tg):
+    """2^32 lanes of 256 to a row, and five rows; all of them against the definition."""
+    M, K = (1 << 24) + 5, 8
+    x = torch.empty(M, K, device="cuda", dtype=BF).normal_(generator=gen(1))
+    q, scale = torch.full((M + 1, 16), 99, device="cuda", dtype=I8), torch.full((M + 1,), -1.0, device="cuda")
+    tg.tg_quantize_i8(x, q[:M, :K], scale[:M])
+    for i in range(0, M, 1 << 22):
+        wq, ws = quantized(x[i:i + (1 << 22)])
+        n = i + len(ws)
+        assert torch.equal(scale[i:n].cpu(), ws) and torch.equal(q[i:n, :K].cpu(), wq), i
+    assert float(scale[M]) == -1.0
+    assert bool((q[:, K:] == 99).all()) and bool((q[M] == 99).all())
+
+
 def test_quantized_values_that_are_not_finite_and_small_ones(tg):
     x = torch.randn(5, 300, device="cuda")
     x[0, 7] = float("nan")

@@ -12,6 +12,7 @@ tg_status i8_linear_f32(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_
 tg_status i8_linear_f16(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_bytes, hipStream_t s);
 tg_status i8_linear_bf16(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_bytes, hipStream_t s);
 
+constexpr int64_t kQuantRows = 1 << 22;  // rows of a launch at most (a launch has less than 2^32 lanes)
 constexpr int64_t kQuantFew = 512;  // rows up to which a row takes 1024 lanes
 // q past this leaves the L2s before a product reads it, and is stored with the
 // non-temporal hint (8192 x 10240 bf16 49.3 -> 46.5 us, its product as it was;
@@ -173,8 +174,16 @@ __global__ __launch_bounds__(T) void quantize_rows(QuantArgs p)
 // 1024 lanes of one or two pieces.  More rows take 256 lanes, holding as much
 // of a row as it has up to eight pieces.
 template <int O>
-static void quantize_launch(const QuantArgs& a, hipStream_t s)
+static void quantize_launch(QuantArgs a, hipStream_t s)
 {
+    for (; a.M > kQuantRows; a.M -= kQuantRows) {
+        QuantArgs part = a;
+        part.M = kQuantRows;
+        quantize_launch<O>(part, s);
+        a.x = (const uint8_t*)a.x + kQuantRows * a.ldx * (O == O_F32 ? 4 : 2);
+        a.q += kQuantRows * a.ldq;
+        a.scale += kQuantRows;
+    }
     const dim3 grid((uint32_t)a.M);
     const int64_t pieces = (a.K + Piece<O>::N - 1) / Piece<O>::N;
     if (a.M <= kQuantFew) {
