@@ -68,9 +68,9 @@ int64_t tg_linear_xent_workspace_bytes(tg_input in, int64_t M, int64_t V, int64_
  * The workspace is required (with an output given and V > 0).  Its size sets
  * the pieces: the library takes as few as fit it, and adds dX in another
  * order where that changes them.  workspace_bytes(piece) reports what pieces
- * of `piece` columns need (rounded up to a multiple of 256), or one piece where
- * that is less; piece 0 stands for the size past which more gives nothing,
- * piece 1 for the least. */
+ * of `piece` columns need (rounded up to a multiple of 256), for any ldw;
+ * piece 0 stands for the size past which more gives nothing, piece 1 for the
+ * least. */
 tg_status tg_linear_xent_backward(tg_input in, int64_t M, int64_t V, int64_t D,
                                   const void *x, int64_t ldx, const void *W, int64_t ldw,
                                   float scale, const int64_t *targets, int64_t ignore_index, float z_loss,

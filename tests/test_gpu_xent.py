@@ -136,6 +136,21 @@ def test_gradients(tg, M, V, D, piece, dtype, dw_dtype):
     backward_case(tg, M, V, D, dtype, dw_dtype, piece, weighted=piece == 0, counted=M % 2 == 1)
 
 
+def test_gradients_of_a_weight_whose_rows_lie_far_apart(tg, monkeypatch):
+    """4500 rows over 2 GiB take two pieces, and dx's sums, in a workspace whose query had one piece in mind."""
+    M, V, D = 160, 4500, 1256
+    w = torch.empty(V, 240000, device="cuda", dtype=BF)[:, :D]
+    near = problem
+
+    def far(*a):
+        x, v, target = near(*a)
+        return x, w.copy_(v), target
+
+    monkeypatch.setitem(globals(), "problem", far)
+    for piece in (0, 1, 4608):
+        backward_case(tg, M, V, D, BF, F32, piece)
+
+
 def test_gradients_of_small_probabilities_and_large_factors(tg):
     """fp16: factors far from 1 (loss scaling, a mean over many rows) do not cost the small probabilities their digits."""
     for gs in (65536.0, 2.0 ** -8):

@@ -50,7 +50,7 @@ extern "C" int64_t tg_linear_xent_backward_workspace_bytes(tg_input in_arg, int6
         return -1;
     if (V == 0 || !dims_fit(M, V, D) || !width_fits(D, D))
         return 0;
-    const int64_t n = xent_bwd_bytes(M, V, D, D, piece);
+    const int64_t n = xent_bwd_bytes(M, V, D, piece);
     return n < 0 ? 0 : n;
 }
 
@@ -144,7 +144,7 @@ extern "C" tg_status tg_linear_xent_backward(tg_input in_arg, int64_t M, int64_t
     if (st == TG_OK && dW != nullptr)
         st = check_mat(dW, V, D, lddw, out_bytes(dw_dtype));
     if (st == TG_OK)
-        st = check_ws(workspace, workspace_bytes, nothing || workspace == nullptr ? 0 : xent_bwd_bytes(M, V, D, ldw, 1));
+        st = check_ws(workspace, workspace_bytes, nothing || workspace == nullptr ? 0 : xent_bwd_least(M, V, D, ldw));
     if (st == TG_OK && !nothing && workspace == nullptr)
         st = TG_ERR_INVALID_VALUE;
     if (st == TG_OK && (misaligned4(lse) || misaligned4(dloss) || misaligned4(total)))

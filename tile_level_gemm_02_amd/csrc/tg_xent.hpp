@@ -793,16 +793,23 @@ inline XentBwd xent_bwd_plan(int64_t M, int64_t V, int64_t D, int64_t most, int6
     return XentBwd{};
 }
 
-inline int64_t xent_bwd_bytes(int64_t M, int64_t V, int64_t D, int64_t ldw, int64_t piece)
+// Bytes of pieces of `piece` columns, with room for dX's sums also where they
+// make one piece: rows of W far apart may ask for several (xent_most_piece)
+inline int64_t xent_bwd_bytes(int64_t M, int64_t V, int64_t D, int64_t piece)
 {
-    const int64_t most = xent_most_piece(M, V, ldw);
+    const int64_t most = xent_most_piece(M, V, D);
     if (most < 256)
         return -1;
-    piece = piece == 0 || piece > most ? xent_even(V, most) : up(piece, 256);
-    const int64_t bytes = xent_bwd_layout(M, V, D, piece).bytes;
+    const XentBwd b = xent_bwd_layout(M, V, D, piece == 0 || piece > most ? xent_even(V, most) : up(piece, 256));
+    return b.bytes + (b.pieces == 1 && V > 256 ? up(M * up(D, 4) * 4, 256) : 0);
+}
+
+// The least that a call takes: one piece needs no sums, and may take less than several
+inline int64_t xent_bwd_least(int64_t M, int64_t V, int64_t D, int64_t ldw)
+{
+    const int64_t most = xent_most_piece(M, V, ldw), bytes = xent_bwd_layout(M, V, D, 256).bytes;
     if (up(V, 256) > most)
         return bytes;
-    // one piece needs no room for dX's sums, and may take less than several
     const int64_t whole = xent_bwd_layout(M, V, D, up(V, 256)).bytes;
     return whole < bytes ? whole : bytes;
 }
