@@ -259,6 +259,23 @@ def test_a_tensor_past_32_bit_offsets(tg):
         del p, g, m, v
 
 
+def test_more_chunks_than_a_launch_has_room_for(tg):
+    """2^24 chunks of 1024 values, and a part of one: 2^32 lanes and more.  138 GB, every value of which is the same."""
+    n = (1 << 34) + 1000
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("150 GiB of device memory")
+    p, g = torch.full((n,), 0.5, device="cuda"), torch.full((n,), 0.25, device="cuda", dtype=BF)
+    m, v = torch.zeros(n, device="cuda", dtype=torch.uint8), torch.zeros(n, device="cuda", dtype=torch.uint8)
+    sm, sv = torch.zeros(-(-n // BLOCK), device="cuda"), torch.zeros(-(-n // BLOCK), device="cuda")
+    tg.tg_adamw([p], [g], [m.view(F8)], [v.view(F8)], 1, 1e-2, weight_decay=0.0, exp_avg_scales=[sm], exp_avg_sq_scales=[sv])
+    assert abs(float(p[0]) - 0.49) < 1e-6
+    for t in (p, m, v, sm, sv):
+        first = t[:1].clone()
+        assert all(bool((t[i:i + (1 << 31)] == first).all()) for i in range(0, len(t), 1 << 31))
+    del p, g, m, v, sm, sv, t
+    torch.cuda.empty_cache()
+
+
 def test_wrong_tensors_are_refused(tg):
     z = lambda n, dtype=F32: torch.zeros(n, device="cuda", dtype=dtype)  # noqa: E731
     p, f8, s = z(300), z(300, torch.uint8).view(F8), z(2)

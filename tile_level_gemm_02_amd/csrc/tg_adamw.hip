@@ -27,7 +27,8 @@
 namespace tg {
 
 constexpr int kAdamTensors = 48;       // descriptors per launch (under 4 KiB of kernel arguments)
-constexpr int64_t kAdamGrid = 1 << 24; // workgroups of a launch at most
+constexpr int64_t kAdamGrid = 1 << 23;  // workgroups of a launch at most
+static_assert(kAdamGrid * 256 <= 0x7FFFFFFF + (int64_t)1, "a launch has less than 2^32 lanes");
 constexpr int kAdamBlock = 256;        // elements per scale of 8-bit states
 constexpr float kE4m3Max = 448.0f, kE4m3Step = 0.001953125f;  // largest and smallest positive value
 constexpr float kAdamTiny = 7.888609052210118e-31f;           // 2^-100
@@ -442,7 +443,7 @@ extern "C" tg_status tg_adamw(int64_t count, const tg_adamw_tensor* tensors, int
                 if (t.n == 0 || t.p_dtype != p || t.g_dtype != g || (t.master != nullptr) != master)
                     continue;
                 const int64_t c = (t.n + chunk - 1) / chunk;
-                if (chunks + c > 0xFFFFFFFF)
+                if (chunks + c > 0x7FFFFFFF)  // (a chunk's number and a grid more fit in 32 bits)
                     break;
                 const int k = a.count++;
                 a.p[k] = t.param;
