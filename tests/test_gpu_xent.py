@@ -90,7 +90,7 @@ def check_forward(tg, M, V, D, dtype, scale=0.9, z=1e-3, seed=1):
 @pytest.mark.parametrize("M,V,D", [(1, 1, 8), (1, 17, 64), (2, 1000, 136), (8, 4097, 200), (9, 8300, 72), (16, 333, 1032), (17, 1500, 264),
                                    (32, 65, 8), (33, 63, 64), (40, 200, 520), (65, 129, 72), (130, 5003, 136), (1270, 1281, 72),
                                    (2300, 2290, 136), (3580, 3570, 72), (777, 32003, 136), (4600, 5300, 72), (4352, 4352, 64),
-                                   (4360, 4350, 136)])
+                                   (4360, 4350, 136), (140000, 40, 8)])
 @pytest.mark.parametrize("dtype", [BF, F16])
 def test_loss(tg, M, V, D, dtype):
     check_forward(tg, M, V, D, dtype)
@@ -129,6 +129,8 @@ def backward_case(tg, M, V, D, dtype, dw_dtype, piece=0, weighted=False, counted
                                          (512, 9000, 1032, 4096), (2300, 2290, 136, 0), (4100, 513, 256, 0), (4352, 4400, 64, 0),
                                          # one piece, which has no sums of dx, needs less than two
                                          (160, 452, 1256, 512), (160, 452, 1256, 1),
+                                         # the rows' largest factor in several passes of its workgroups
+                                         (140000, 40, 8, 0),
                                          # dx's K, the vocabulary, over workgroups whose partial tiles a kernel adds; over pieces as well
                                          (600, 70003, 264, 0), (600, 70003, 264, 65536), (129, 131080, 520, 0)])
 @pytest.mark.parametrize("dtype,dw_dtype", [(BF, BF), (BF, F32), (F16, F16), (F16, F32)])

@@ -194,6 +194,30 @@ __device__ __forceinline__ void join_pair(float& top, float& sum, float t, float
     top = m;
 }
 
+// Arrivals at one word take 12 ns each, whichever workgroups make them (131072
+// rows 102 us, 92 of them so).  Many workgroups therefore arrive at words on
+// lines of their own, and the last at each of these at the first word.  All
+// words are left zero.
+constexpr uint32_t kJoinGroups = 64, kJoinMany = 256;
+static_assert((kJoinGroups + 1) * 256 <= kSplitCounterBytes, "words 256 bytes apart");
+
+__device__ __forceinline__ bool arrive(uint32_t* word, uint32_t n)
+{
+    if (__hip_atomic_fetch_add(word, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != n - 1u)
+        return false;
+    __hip_atomic_exchange(word, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// by one lane of each workgroup, whose stores are complete: true in the last
+__device__ __forceinline__ bool last_arrival(uint32_t* counters)
+{
+    if (gridDim.x <= kJoinMany)
+        return arrive(counters, gridDim.x);
+    const uint32_t g = blockIdx.x % kJoinGroups, n = (gridDim.x - g + kJoinGroups - 1u) / kJoinGroups;
+    return arrive(counters + 64u * (1u + g), n) && arrive(counters, kJoinGroups);
+}
+
 // The slots of R rows per workgroup, 256 / R lanes to a row, several loads
 // ahead of their arithmetic; lanes and waves are added in a fixed order.  Bound
 // by the slots' reads (8 bytes for every 64 columns of every row).
@@ -282,23 +306,47 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
         __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x, a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        last = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1u;
+        last = last_arrival(p.counter);
     }
     __syncthreads();
-    if (!last || tid >= 64u)
+    constexpr uint32_t LANES = R == 1 ? 64u : 256u;  // (one row a workgroup: 64 slots at most)
+    if (!last || tid >= LANES)
         return;
     double a = 0.0, b = 0.0;
-    for (uint32_t k = tid; k < gridDim.x; k += 64u) {
-        a += __hip_atomic_load(p.sums + 2 * (size_t)k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        b += __hip_atomic_load(p.sums + 2 * (size_t)k + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    constexpr uint32_t AHEAD = R == 1 ? 1u : 8u;  // loads of a lane in flight
+    for (uint32_t k0 = tid; k0 < gridDim.x; k0 += LANES * AHEAD) {
+        double u[AHEAD], w[AHEAD];
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            const uint32_t k = k0 + i * LANES;
+            u[i] = w[i] = 0.0;
+            if (k < gridDim.x) {
+                u[i] = __hip_atomic_load(p.sums + 2 * (size_t)k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                w[i] = __hip_atomic_load(p.sums + 2 * (size_t)k + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            a += u[i];
+            b += w[i];
+        }
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
         a += __shfl_down(a, d, 64);
         b += __shfl_down(b, d, 64);
     }
+    if constexpr (LANES > 64u) {
+        __shared__ double waves[2][4];
+        if (tid % 64u == 0u) {
+            waves[0][tid / 64u] = a;
+            waves[1][tid / 64u] = b;
+        }
+        __syncthreads();
+        a = waves[0][0] + waves[0][1] + waves[0][2] + waves[0][3];
+        b = waves[1][0] + waves[1][1] + waves[1][2] + waves[1][3];
+    }
     if (tid == 0u) {
-        __hip_atomic_exchange(p.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         p.total[0] = (float)a;
         p.total[1] = (float)b;
     }
@@ -484,23 +532,44 @@ struct XentRowsArgs {
     int64_t ignore;
     float z, scale, grad_scale, lift;  // lift: 2^12 for fp16, 1 for bf16
     const float *lse, *dloss, *total;
-    const float* most;  // the largest row factor (xent_most), or null: 1
+    const float* most;  // the largest row factors (xent_most), or null: 1
+    int32_t most_n;     // how many
     XentRow* rows;
     float* factor;
 };
 
-// The largest factor of a row that counts, by one workgroup
+constexpr int kXentMost = 32;  // workgroups of xent_most at most: a lane of xent_rows' waves for each
+
+// The largest factor of the rows that count, one for each workgroup; a lane has
+// four rows' loads in flight (131072 rows in one workgroup, a row at a time: 130 us)
 template <int = 0>
 __global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
 {
     __shared__ float red[16];
     const uint32_t tid = threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * 1024;
     float most = 0.0f;
-    for (int64_t i = tid; i < p.M; i += 1024)
-        if (p.target[i] != p.ignore) {
-            const float b = p.dloss != nullptr ? __builtin_fabsf(p.dloss[i]) : 1.0f;
-            most = max2(most, max2(b, b * __builtin_fabsf(1.0f + 2.0f * p.z * p.lse[i])));
+    for (int64_t i0 = (int64_t)blockIdx.x * 1024 + tid; i0 < p.M; i0 += 4 * step) {
+        float b[4], lse[4];
+        bool counts[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * step;
+            b[u] = 1.0f;
+            lse[u] = 0.0f;
+            counts[u] = false;
+            if (i < p.M) {
+                counts[u] = p.target[i] != p.ignore;
+                if (p.dloss != nullptr)
+                    b[u] = __builtin_fabsf(p.dloss[i]);
+                lse[u] = p.lse[i];
+            }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (counts[u])
+                most = max2(most, max2(b[u], b[u] * __builtin_fabsf(1.0f + 2.0f * p.z * lse[u])));
+    }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         most = max2(most, __shfl_xor(most, d, 64));
@@ -511,7 +580,7 @@ __global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
     for (int k = 0; k < 16; ++k)
         most = max2(most, red[k]);
     if (tid == 0u)
-        *out = most;
+        out[blockIdx.x] = most;
 }
 
 // Each row's numbers relative to a power of two at or above the largest; what
@@ -521,7 +590,14 @@ __global__ __launch_bounds__(256) void xent_rows(XentRowsArgs p)
 {
     // 2^e >= most, within fp32's normal numbers (infinity, and none at all: 1)
     int e = 0;
-    const float most = p.most != nullptr ? *p.most : 1.0f;
+    float most = 1.0f;
+    if (p.most != nullptr) {
+        const int lane = (int)(threadIdx.x % 64u);
+        most = lane < p.most_n ? p.most[lane] : 0.0f;
+#pragma unroll
+        for (int d = kXentMost; d > 0; d >>= 1)
+            most = max2(most, __shfl_xor(most, d, 64));
+    }
     if (most > 0.0f && most < INFINITY && most != 1.0f) {
         (void)frexpf(most, &e);
         e = e < -100 ? -100 : e;
@@ -883,11 +959,13 @@ tg_status xent_backward(const XentCall& q)
     float* const factor = (float*)(ws + b.factor);
     float* const sums = (float*)(ws + b.sums);
     const int64_t lds = up(q.D, 4);
-    XentRowsArgs r{q.M, q.V, q.target, q.ignore, q.z, q.scale, q.grad_scale, E == E_F16 ? 4096.0f : 1.0f, q.lse, q.dloss, q.total, nullptr, rows, factor};
+    XentRowsArgs r{q.M, q.V, q.target, q.ignore, q.z, q.scale, q.grad_scale, E == E_F16 ? 4096.0f : 1.0f, q.lse, q.dloss, q.total, nullptr, 0, rows, factor};
     // factors of the rows' own are taken relative to the largest; 1 + 2 z lse is
     // near enough to 1 for bf16's range
     if (q.dloss != nullptr || (E == E_F16 && q.z != 0.0f)) {
-        hipLaunchKernelGGL(xent_most<>, dim3(1), dim3(1024), 0, q.s, r, factor + 1);
+        const int64_t groups = (q.M + 1023) / 1024;
+        r.most_n = (int32_t)(groups > kXentMost ? kXentMost : groups + (groups == 0));
+        hipLaunchKernelGGL(xent_most<>, dim3((uint32_t)r.most_n), dim3(1024), 0, q.s, r, factor + 1);
         r.most = factor + 1;
     }
     hipLaunchKernelGGL(xent_rows<>, dim3((uint32_t)((q.M + 255) / 256 + (q.M == 0))), dim3(256), 0, q.s, r);
