@@ -40,7 +40,8 @@ extern "C" {
  * maximum and the sum of its columns.  A logit of NaN or infinity makes its
  * row's lse and loss NaN (-infinity counts as probability 0).
  * D has to be a multiple of 8, scale and z_loss finite; V > 0 unless M == 0.
- * The workspace is required when M > 0. */
+ * The workspace is required when M > 0 or total is given (with M == 0 total
+ * receives two zeros); its query holds for M == 0 too. */
 tg_status tg_linear_xent(tg_input in, int64_t M, int64_t V, int64_t D,
                          const void *x, int64_t ldx, const void *W, int64_t ldw,
                          float scale, const int64_t *targets, int64_t ignore_index, float z_loss,

@@ -39,7 +39,7 @@ extern "C" int64_t tg_linear_xent_workspace_bytes(tg_input in_arg, int64_t M, in
 {
     if (M < 0 || V < 0 || D < 0 || !type_ok(abi_int(in_arg)))
         return -1;
-    if (!dims_fit(M, V, D) || !width_fits(D, D))
+    if (!dims_fit(M, V, D) || (M > 0 && !width_fits(D, D)))
         return 0;
     return xent_fwd_layout(M, V, kFusedSkinnyRows<E_BF16>).bytes;
 }
@@ -85,15 +85,13 @@ extern "C" tg_status tg_linear_xent(tg_input in_arg, int64_t M, int64_t V, int64
     q.s = (hipStream_t)stream;
     tg_status st = xent_check(q);
     if (st == TG_OK)
-        st = check_ws(workspace, workspace_bytes, M == 0 ? 0 : tg_linear_xent_workspace_bytes(in_arg, M, V, D));
+        st = check_ws(workspace, workspace_bytes, M == 0 && total == nullptr ? 0 : tg_linear_xent_workspace_bytes(in_arg, M, V, D));
     if (st == TG_OK && (misaligned4(loss) || misaligned4(lse) || misaligned4(total)))
         st = TG_ERR_MISALIGNED;
     if (st != TG_OK || (M == 0 && total == nullptr))
         return st;
-    if (M == 0) {  // two zeros: written by a workgroup of no rows, which needs a counter and a slot
-        if (workspace == nullptr || workspace_bytes < xent_fwd_layout(0, 0, 0).bytes + 256)
-            return TG_ERR_INVALID_VALUE;
-    }
+    if (workspace == nullptr)  // (M == 0: a workgroup of no rows writes total's zeros)
+        return TG_ERR_INVALID_VALUE;
     return in == TG_IN_F16 ? xent_forward_f16(q) : xent_forward_bf16(q);
 }
 

@@ -651,7 +651,8 @@ inline XentFwd xent_fwd_layout(int64_t M, int64_t V, int64_t few)
     f.part = kSplitCounterBytes;
     f.picked = up(f.part + f.slots * M * 8, 256);
     f.sums = up(f.picked + M * 4, 256);
-    f.bytes = up(f.sums + (M + f.join_rows - 1) / f.join_rows * 16, 256);
+    // (a slot of the sums without rows as well: their workgroup writes the total)
+    f.bytes = up(f.sums + (M == 0 ? 1 : (M + f.join_rows - 1) / f.join_rows) * 16, 256);
     return f;
 }
 
