@@ -184,8 +184,13 @@ struct XentJoinArgs {
     float z;
     float *loss, *lse, *total;
     uint32_t* counter;
-    double* sums;  // [workgroups][2]: losses and counted rows
+    double* sums;    // [workgroups][2]: losses and counted rows
+    uint32_t first;  // workgroups of the launches before
+    int32_t more;    // launches follow, the last of which adds the sums
 };
+
+// Workgroups of a launch at most (of 256 lanes: a launch has less than 2^32)
+constexpr int64_t kJoinGrid = 1 << 23;
 
 __device__ __forceinline__ void join_pair(float& top, float& sum, float t, float s)
 {
@@ -229,7 +234,8 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
     __shared__ double own[2][R];
     __shared__ bool last;
     const uint32_t tid = threadIdx.x, r = tid % R, part = tid / R;
-    const int64_t row = (int64_t)blockIdx.x * R + r;
+    const uint32_t group = p.first + blockIdx.x;
+    const int64_t row = (int64_t)group * R + r;
     float top = -INFINITY, sum = 0.0f;
     if (row < p.M) {
         for (int64_t s0 = part; s0 < p.slots; s0 += (int64_t)T * B) {
@@ -303,10 +309,10 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
             a += own[0][k];
             b += own[1][k];
         }
-        __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x, a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(p.sums + 2 * (size_t)blockIdx.x + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(p.sums + 2 * (size_t)group, a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(p.sums + 2 * (size_t)group + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        last = last_arrival(p.counter);
+        last = p.more == 0 && last_arrival(p.counter);
     }
     __syncthreads();
     constexpr uint32_t LANES = R == 1 ? 64u : 256u;  // (one row a workgroup: 64 slots at most)
@@ -314,13 +320,14 @@ __global__ __launch_bounds__(256) void xent_join(XentJoinArgs p)
         return;
     double a = 0.0, b = 0.0;
     constexpr uint32_t AHEAD = R == 1 ? 1u : 8u;  // loads of a lane in flight
-    for (uint32_t k0 = tid; k0 < gridDim.x; k0 += LANES * AHEAD) {
+    const uint32_t groups = p.first + gridDim.x;
+    for (uint32_t k0 = tid; k0 < groups; k0 += LANES * AHEAD) {
         double u[AHEAD], w[AHEAD];
 #pragma unroll
         for (uint32_t i = 0; i < AHEAD; ++i) {
             const uint32_t k = k0 + i * LANES;
             u[i] = w[i] = 0.0;
-            if (k < gridDim.x) {
+            if (k < groups) {
                 u[i] = __hip_atomic_load(p.sums + 2 * (size_t)k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 w[i] = __hip_atomic_load(p.sums + 2 * (size_t)k + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
@@ -766,11 +773,16 @@ tg_status xent_forward(const XentCall& q)
     j.total = q.total_out;
     j.counter = (uint32_t*)ws;
     j.sums = (double*)(ws + f.sums);
-    const int64_t grid = q.M == 0 ? 1 : (q.M + f.join_rows - 1) / f.join_rows;
-    if (f.join_rows == 1)
-        hipLaunchKernelGGL(xent_join<1>, dim3((uint32_t)grid), dim3(256), 0, q.s, j);
-    else
-        hipLaunchKernelGGL(xent_join<16>, dim3((uint32_t)grid), dim3(256), 0, q.s, j);
+    const int64_t groups = q.M == 0 ? 1 : (q.M + f.join_rows - 1) / f.join_rows;
+    for (int64_t first = 0; first < groups; first += kJoinGrid) {
+        const uint32_t grid = (uint32_t)(groups - first < kJoinGrid ? groups - first : kJoinGrid);
+        j.first = (uint32_t)first;
+        j.more = first + grid < groups;
+        if (f.join_rows == 1)
+            hipLaunchKernelGGL(xent_join<1>, dim3(grid), dim3(256), 0, q.s, j);
+        else
+            hipLaunchKernelGGL(xent_join<16>, dim3(grid), dim3(256), 0, q.s, j);
+    }
     return launched();
 }
 
