@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from _train_ref import within, xent
+from _train_ref import U, adds, logits, within, xent
 from test_gpu_xent import BF, F16, IGNORE, MARK, free, gen, space
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +58,58 @@ def test_more_rows_than_a_launch_of_the_join_has_lanes_for(tg):
     again = torch.empty(2, device="cuda")
     tg.tg_linear_xent(x, w, target, None, None, again, scale=0.9, ignore_index=IGNORE, workspace=ws)
     assert torch.equal(again, total)
+
+
+def far_ends(tg, M, V, D, rows, ends, room=24):
+    """The loss of M x V logits at `rows`, whose targets take the columns in `ends` and others, against sums in 64 bits."""
+    need = tg.tg_linear_xent_workspace_bytes(BF, M, V, D)
+    if torch.cuda.mem_get_info()[0] < need + 2 * D * (M + V) + (room << 30):
+        pytest.skip("device memory")
+    print(f"xent {M}x{V}x{D}", flush=True)
+    x = torch.empty(M, D, device="cuda", dtype=BF).normal_(generator=gen(1))
+    w = torch.empty(V, D, device="cuda", dtype=BF)
+    for i in range(0, V, 1 << 26):
+        w[i:i + (1 << 26)].normal_(generator=gen(2))
+    w[-1] = x[rows[0]] * 2  # (a last column that its row's sum would miss)
+    target = torch.randint(0, V, (M,), device="cuda", generator=gen(3))
+    rows = torch.tensor(rows, device="cuda")
+    target[rows] = torch.tensor([ends[i % len(ends)] for i in range(len(rows))], device="cuda")
+    target[rows[-1]] = IGNORE
+    loss, lse, total = (torch.empty(n, device="cuda") for n in (M, M, 2))
+    ws = torch.zeros(need // 4, dtype=torch.int32, device="cuda")
+    tg.tg_linear_xent(x, w, target, loss, lse, total, ignore_index=IGNORE, workspace=ws)
+    free(ws)
+    del ws
+    # rows' sums over parts of the vocabulary; the bound of each logit and of its exponential as _train_ref's, their largest
+    part, a = max(1 << 16, (1 << 28) // len(rows)), x[rows]
+    sums, off, tops = [], 0.0, 0.0
+    for i in range(0, V, part):
+        t, dt = logits(a, w[i:i + part], 1.0)
+        sums.append(torch.logsumexp(t, 1))
+        off, tops = torch.clamp(dt.amax(1), min=off), torch.clamp(t.abs().amax(1), min=tops)
+    lse64 = torch.logsumexp(torch.stack(sums), 0)
+    de = off + 4 * U * (tops + lse64.abs()) + 4 * U + 2 * adds(V) * U + 2 * U * lse64.abs()
+    within(lse[rows], lse64, de, "lse")
+    counts = target[rows] != IGNORE
+    tt = (a.double() * w[target[rows].clamp(min=0)].double()).sum(1)
+    within(loss[rows], torch.where(counts, lse64 - tt, 0.0), de + off + 4 * U * (lse64.abs() + tt.abs()), "loss")
+    # all of them: the total is their sum
+    assert float(total[1]) == float(torch.tensor(float((target != IGNORE).sum())))
+    want = float(loss.double().sum())
+    assert abs(float(total[0]) - want) <= 2.0 ** -23 * want and bool(loss.isfinite().all())
+
+
+def test_more_tiles_than_a_launch_has_lanes_for(tg):
+    """2^39 logits and more: the rows go in two launches of 2^23 tiles of 512 lanes, the second from row 8355840 on."""
+    M, V = (1 << 23) + 301, (1 << 16) + 64
+    cut = 8355840
+    rows = list(range(40)) + list(range(cut - 40, cut + 40)) + list(range(M - 40, M))
+    far_ends(tg, M, V, 8, rows, [0, V - 1, V - 2, 65535, 65536, 777])
+
+
+def test_wide_vocabularies(tg):
+    """Few rows against more columns than the few-rows kernel's launch has lanes for, and more than 2^30 columns, which go in parts."""
+    V = (1 << 27) + 77
+    far_ends(tg, 3, V, 8, [0, 1, 2], [V - 1, 0])
+    V = (1 << 30) + 300
+    far_ends(tg, 33, V, 8, list(range(33)), [V - 1, 0, (1 << 30) - 1, 1 << 30, (1 << 30) + 63, (1 << 30) + 64, 12345])

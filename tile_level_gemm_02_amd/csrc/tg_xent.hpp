@@ -41,8 +41,10 @@ struct XentRow {
 struct XentOut {
     float c, scale;
     const int64_t* target;
-    f32x2_t* part;   // [slot][M]: largest t (base 2) and sum of 2^(t - largest) over the slot's columns
-    float* picked;   // [M]: t of the target
+    f32x2_t* part;   // [slot][rows]: largest t (base 2) and sum of 2^(t - largest) over the slot's columns
+    float* picked;   // [rows]: t of the target
+    int64_t rows;    // of the call, of which a launch may have a part
+    int64_t v0;      // first column of the launch's part of the vocabulary
 };
 
 // One value per lane reduced over the lanes that hold the same row (RBK apart:
@@ -90,7 +92,7 @@ struct XentFwdArgs : TileArgs {
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int64_t k = target[i] - col0;
+            const int64_t k = target[i] - x.v0 - col0;
             at[i] = k >= 0 && k < left ? (int)k : -1;
         }
         // WHOLE: all columns are there and c is not negative, so that the largest
@@ -122,7 +124,7 @@ struct XentFwdArgs : TileArgs {
                 sum = over_row_lanes<RBK>(sum, add2);
                 if (row < M) {
                     if (lg == 0)
-                        x.part[slot * M + row] = f32x2_t{top, sum};
+                        x.part[slot * x.rows + row] = f32x2_t{top, sum};
                     if (at[i] >= 0 && at[i] / 4 % G == lg) {
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
@@ -167,7 +169,7 @@ struct XentSkinnyArgs : SkinnyArgs {
         if (!in || col16 >= N)
             return;
         if (lane < 16u)
-            x.part[col16 / 16 * M + row] = f32x2_t{top, sum};
+            x.part[col16 / 16 * x.rows + row] = f32x2_t{top, sum};
         const int64_t at = x.target[row] - col;
         if (at >= 0 && at < left)
             x.picked[row] = (at == 0 ? a[0] : at == 1 ? a[1] : at == 2 ? a[2] : a[3]) * x.scale;
@@ -633,11 +635,12 @@ __global__ __launch_bounds__(256) void xent_rows(XentRowsArgs p)
 // --------------------------------------------------------------- host side
 inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// forward: the skinny kernel's rows, as for tg_linear
+// forward: the skinny kernel's rows, as for tg_linear (a launch has less than 2^32 lanes)
 template <int E>
 bool xent_skinny(int64_t M, int64_t D, int64_t ldx, int64_t ldw, int64_t V)
 {
-    return M <= kFusedSkinnyRows<E> && D > 0 && skinny_offsets_fit(D, ldx, ldw, SkinnyCfg::RING, fused_cg(M, V));
+    return M <= kFusedSkinnyRows<E> && D > 0 && fused_skinny_blocks(M, V) * 64 * SkinnyCfg::WAVES <= 0x7FFFFFFF &&
+           skinny_offsets_fit(D, ldx, ldw, SkinnyCfg::RING, fused_cg(M, V));
 }
 
 struct XentFwd {
@@ -698,12 +701,42 @@ void launch_xent_skinny(const XentSkinnyArgs& a, int64_t blocks, hipStream_t s)
                        dim3(64 * G::WAVES), 0, s, a);
 }
 
+// A part of the forward product, of up to kXentTiles tiles
+template <int E>
+tg_status xent_logits(XentFwdArgs a, hipStream_t s)
+{
+    // tiles whose waves hold 64 columns: no 64 x 64 ones
+    const NtPlan p = plan_nt<E, B_KCONTIG>(a.M, a.N, a.K, false);
+    if (p.tile == 256 && p.tn == 128)
+        return launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(a, 1, s);
+    if (p.tile == 256 && p.tail == kTailNone)
+        return launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, s);
+    if (p.tile == 256) {
+        XentFwdArgs b = a;
+        const int64_t rest = n_tiles<256, 256>(a.M, a.N) - p.dp;
+        a.dp = (uint32_t)p.dp;
+        const tg_status st = launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, s, p.dp);
+        if (st != TG_OK)
+            return st;
+        b.sub256 = (uint32_t)p.dp + 1u;
+        return p.tail == kTailWide ? launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(b, 1, s, 2 * rest)
+                                   : launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(b, 1, s, 4 * rest);
+    }
+    if (n_tiles<128, 128>(a.M, a.N) <= 256)
+        return launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(a, 1, s);
+    return launch_nt<E, O_F32, 128, 128, B_KCONTIG, 4, EPI_OWN, A_KCONTIG>(a, 1, s);
+}
+
+// Tiles of 512 lanes in a launch (which has less than 2^32) of the forward
+// product, and columns: past 2^39 logits it goes in parts
+constexpr int64_t kXentTiles = (1 << 23) - 1, kXentWide = (int64_t)1 << 30;
+
 template <int E>
 tg_status xent_forward(const XentCall& q)
 {
     const XentFwd f = xent_fwd_layout(q.M, q.V, kFusedSkinnyRows<E>);
     uint8_t* const ws = (uint8_t*)q.ws;
-    XentOut o{xent_c(q.scale), q.scale, q.target, (f32x2_t*)(ws + f.part), (float*)(ws + f.picked)};
+    XentOut o{xent_c(q.scale), q.scale, q.target, (f32x2_t*)(ws + f.part), (float*)(ws + f.picked), q.M, 0};
     int64_t slots = f.slots;
     if (q.M == 0) {
         // (only the total, of no rows)
@@ -718,8 +751,6 @@ tg_status xent_forward(const XentCall& q)
         a.ldb = q.ldw;
         a.x = o;
         const int64_t blocks = fused_skinny_blocks(q.M, q.V);
-        if (blocks > 0x7FFFFFFF)
-            return TG_ERR_NOT_SUPPORTED;
         if (q.M <= 8)
             launch_xent_skinny<E, 1, 1>(a, blocks, q.s);
         else if (fused_cg(q.M, q.V) == 1)
@@ -728,36 +759,25 @@ tg_status xent_forward(const XentCall& q)
             launch_xent_skinny<E, 2, 2>(a, blocks, q.s);
     } else {
         slots = (q.V + kXentCols - 1) / kXentCols;
-        XentFwdArgs a{};
-        set_product(a, q.M, q.V, q.D, q.x, q.ldx, q.W, q.ldw, nullptr, 0, 1.0f);
-        a.x = o;
-        a.group_m = 4;
-        a.splits = 1;
-        if (!nt_eligible<E>(a))
-            return TG_ERR_NOT_SUPPORTED;
-        // tiles whose waves hold 64 columns: no 64 x 64 ones
-        const NtPlan p = plan_nt<E, B_KCONTIG>(q.M, q.V, q.D, false);
-        tg_status st = TG_OK;
-        if (p.tile == 256 && p.tn == 128) {
-            st = launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(a, 1, q.s);
-        } else if (p.tile == 256 && p.tail == kTailNone) {
-            st = launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, q.s);
-        } else if (p.tile == 256) {
-            XentFwdArgs b = a;
-            const int64_t rest = n_tiles<256, 256>(a.M, a.N) - p.dp;
-            a.dp = (uint32_t)p.dp;
-            st = launch_nt<E, O_F32, 256, 256, B_KCONTIG, 5, EPI_OWN, A_KCONTIG>(a, 1, q.s, p.dp);
-            b.sub256 = (uint32_t)p.dp + 1u;
-            if (st == TG_OK)
-                st = p.tail == kTailWide ? launch_nt<E, O_F32, 256, 128, B_KCONTIG, kWideNH, EPI_OWN, A_KCONTIG>(b, 1, q.s, 2 * rest)
-                                         : launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(b, 1, q.s, 4 * rest);
-        } else if (n_tiles<128, 128>(a.M, a.N) <= 256) {
-            st = launch_nt<E, O_F32, 128, 128, B_KCONTIG, 8, EPI_OWN, A_KCONTIG>(a, 1, q.s);
-        } else {
-            st = launch_nt<E, O_F32, 128, 128, B_KCONTIG, 4, EPI_OWN, A_KCONTIG>(a, 1, q.s);
-        }
-        if (st != TG_OK)
-            return st;
+        const int64_t wide = q.V < kXentWide ? q.V : kXentWide, high = kXentTiles / ((wide + 255) / 256) * 256;
+        for (int64_t v0 = 0; v0 < q.V; v0 += wide)
+            for (int64_t r0 = 0; r0 < q.M; r0 += high) {
+                XentFwdArgs a{};
+                set_product(a, q.M - r0 < high ? q.M - r0 : high, q.V - v0 < wide ? q.V - v0 : wide, q.D, (const uint8_t*)q.x + 2 * r0 * q.ldx, q.ldx,
+                            (const uint8_t*)q.W + 2 * v0 * q.ldw, q.ldw, nullptr, 0, 1.0f);
+                a.x = o;
+                a.x.target += r0;
+                a.x.part += v0 / kXentCols * q.M + r0;
+                a.x.picked += r0;
+                a.x.v0 = v0;
+                a.group_m = 4;
+                a.splits = 1;
+                if (!nt_eligible<E>(a))
+                    return TG_ERR_NOT_SUPPORTED;
+                const tg_status st = xent_logits<E>(a, q.s);
+                if (st != TG_OK)
+                    return st;
+            }
     }
     XentJoinArgs j{};
     j.M = q.M;
