@@ -139,7 +139,17 @@ void launch_i8_skinny(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipSt
                        dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * WAVES), 0, s, a);
 }
 
-constexpr int kI8MostRing = 4;
+constexpr int kI8MostRing = 4, kI8MostWaves = 8;
+
+// Whether the few-rows kernel takes a call (a launch has less than 2^32 lanes)
+inline bool i8_skinny(int64_t M, int64_t N, int64_t K)
+{
+    return M <= kI8SkinnyRows && K > 0 && fused_skinny_blocks(M, N) * 64 * kI8MostWaves <= 0x7FFFFFFF;
+}
+
+// Rows of x or W in a launch at most: its tiles, of 512 lanes each, are fewer
+// than 2^23 then (2 M N bytes of Y fit the memory)
+constexpr int64_t kI8Rows = (int64_t)1 << 30;
 
 // Waves per workgroup and ring slots per wave of the skinny kernel.  An int8
 // row is half the bytes of a 16-bit one, so eight waves get few stages each:
@@ -179,7 +189,7 @@ inline int64_t i8_ws_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M <= 0 || N <= 0 || K <= 0 || K % 16 != 0 || !dims_fit(M, N, K))
         return 0;
-    if (M <= kI8SkinnyRows) {
+    if (i8_skinny(M, N, K)) {
         const int64_t blocks = fused_skinny_blocks(M, N);
         return fused_skinny_ws_bytes(M, N, blocks, fused_split<E_I8>(blocks, K));
     }
@@ -189,7 +199,28 @@ inline int64_t i8_ws_bytes(int64_t M, int64_t N, int64_t K)
 template <int O>
 tg_status i8_linear(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_bytes, hipStream_t s)
 {
-    if (t.M <= kI8SkinnyRows && t.K > 0 && skinny_offsets_fit(t.K, t.lda, t.ldb, kI8MostRing, fused_cg(t.M, t.N))) {
+    if (t.M > kI8Rows || t.N > kI8Rows) {
+        const int64_t ob = O == O_F32 ? 4 : 2;
+        for (int64_t m0 = 0; m0 < t.M; m0 += kI8Rows)
+            for (int64_t n0 = 0; n0 < t.N; n0 += kI8Rows) {
+                TileArgs part = t;
+                I8Epi pe = e;
+                part.M = t.M - m0 < kI8Rows ? t.M - m0 : kI8Rows;
+                part.N = t.N - n0 < kI8Rows ? t.N - n0 : kI8Rows;
+                part.A += m0 * t.lda;
+                part.B += n0 * t.ldb;
+                part.C = (uint8_t*)t.C + (m0 * t.ldc + n0) * ob;
+                pe.R = e.R != nullptr ? (const uint8_t*)e.R + (m0 * e.ldr + n0) * ob : nullptr;
+                pe.bias = e.bias != nullptr ? e.bias + n0 : nullptr;
+                pe.sx = e.sx + m0;
+                pe.sw = e.sw + n0;
+                const tg_status st = i8_linear<O>(part, pe, ws, ws_bytes, s);
+                if (st != TG_OK)
+                    return st;
+            }
+        return TG_OK;
+    }
+    if (i8_skinny(t.M, t.N, t.K) && skinny_offsets_fit(t.K, t.lda, t.ldb, kI8MostRing, fused_cg(t.M, t.N))) {
         I8SkinnyArgs<O> a{};
         a.M = t.M;
         a.N = t.N;
@@ -202,8 +233,6 @@ tg_status i8_linear(const TileArgs& t, const I8Epi& e, void* ws, int64_t ws_byte
         a.ldc = t.ldc;
         a.e = e;
         const int64_t blocks = fused_skinny_blocks(a.M, a.N);
-        if (blocks > 0x7FFFFFFF)
-            return TG_ERR_NOT_SUPPORTED;
         int split = fused_split<E_I8>(blocks, a.K);
         const int64_t need = fused_skinny_ws_bytes(a.M, a.N, blocks, split);
         if (ws == nullptr || need == 0 || need > ws_bytes)
