@@ -97,8 +97,9 @@ int64_t tg_linear_xent_backward_workspace_bytes(tg_input in, int64_t M, int64_t 
  *               sqrt(v) = scale q with a scale per block,
  *   exp_avg_scale, exp_avg_sq_scale : fp32 [ceil(n / 256)], or both NULL (fp32
  *               states).  All tensors of a call have one kind of states.
- *   Held in 8 bits, a state's scale is its block's largest value / 448 (0, and
- *   the block zeros, below 2^-100), its values are rounded to nearest even,
+ *   Held in 8 bits, a state's scale is its block's largest finite value / 448 (0,
+ *   and the block zeros, below 2^-100), its values are rounded to nearest even
+ *   (one that is not finite is held as NaN),
  *   and a nonzero sqrt(v) is kept at e4m3's smallest step or above, so that no
  *   update divides by eps alone.  The update takes the new m and v before they
  *   are rounded.

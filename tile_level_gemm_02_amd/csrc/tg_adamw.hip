@@ -190,15 +190,27 @@ __device__ __forceinline__ float lanes_max(float v)
     return v;
 }
 
-// A block's values as e4m3 and a scale; LIFT: positive ones stay positive
+// A block's values as e4m3 and a scale; LIFT: positive ones stay positive.  The
+// scale is that of the finite values: an infinite one would leave the others as
+// 0 of an infinite scale, NaN to the next step.  It becomes NaN, which e4m3 has
+// and which stays its own.
 template <int V, bool LIFT>
-__device__ __forceinline__ void to_e4m3(const float* v, uint32_t* q, float& scale)
+__device__ __forceinline__ void to_e4m3(float* v, uint32_t* q, float& scale)
 {
-    float top = 0.0f;
+    auto largest = [&]() __attribute__((always_inline)) -> float {
+        float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        top = __builtin_fmaxf(top, LIFT ? v[i] : __builtin_fabsf(v[i]));
-    top = lanes_max<kAdamBlock / V>(top);
+        for (int i = 0; i < V; ++i)
+            top = __builtin_fmaxf(top, LIFT ? v[i] : __builtin_fabsf(v[i]));
+        return lanes_max<kAdamBlock / V>(top);
+    };
+    float top = largest();
+    if (__builtin_amdgcn_ballot_w64(top == INFINITY) != 0) {  // (the whole wave: its lanes exchange their largest)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = __builtin_fabsf(v[i]) == INFINITY ? NAN : v[i];
+        top = largest();
+    }
     top = top < kAdamTiny ? 0.0f : top;
     const float inv = top > 0.0f ? kE4m3Max / top : 0.0f;
     scale = top * (1.0f / kE4m3Max);
