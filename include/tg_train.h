@@ -112,10 +112,9 @@ int64_t tg_linear_xent_backward_workspace_bytes(tg_input in, int64_t M, int64_t 
  *               whose graph moves them on.  step_dev has to hold 1 or more.
  * Tensors must not overlap.  All arithmetic is fp32 on fp32 constants that
  * are computed in fp64; square root and division are off by 2 units in the
- * last place at most together.  The root of a v below 2^-126 is 0, which
- * shows with eps == 0 alone (m' / 0 is infinite).  step >= 1, betas in [0, 1), eps >= 0, max_norm
- * >= 0 (infinity: no clipping), lr and weight_decay finite, else
- * TG_ERR_INVALID_VALUE. */
+ * last place at most together, also of a subnormal v.  step >= 1, betas in
+ * [0, 1), eps >= 0, max_norm >= 0 (infinity: no clipping), lr and weight_decay
+ * finite, else TG_ERR_INVALID_VALUE. */
 typedef struct {
     void *param;
     float *master;

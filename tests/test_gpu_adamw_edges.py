@@ -1,8 +1,10 @@
 """tg_adamw on the GPU at the ends of its numbers: gradients that are not finite
-beside 8-bit states' other values."""
+beside 8-bit states' other values, and second moments below fp32's normal
+numbers."""
 import pytest
 import torch
 
+from _train_ref import U, rounded
 from test_gpu_adamw import BF, F16, F32, Tensor, step_of
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,43 @@ def test_one_gradient_spoils_its_own_element_alone(tg, p, g, master, bad, eight)
     # the spoilt block's other weights are finite after the second step, which reads what the first one held
     w = made[1]["w" if master else "p"].float()[other]
     assert bool(w.isfinite().all())
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-22, 1e-20, 1e-8])
+@pytest.mark.parametrize("p", [F32, BF])
+def test_roots_of_subnormal_second_moments(tg, p, eps):
+    """fp32 states whose v' runs from a few of the smallest steps to normal numbers: the update against its definition of the m' and v'
+    that the step wrote (12 u of it, and the weight's own roundings)."""
+    n = 3000
+    t = Tensor(n, p, F32, False, False, 7)
+    t.t["g"].copy_(10.0 ** torch.linspace(-22, -18, n, device="cuda"))  # v' = 0.05 g^2: 5e-46 (0 or a step) to 5e-38
+    for k in ("m", "v"):
+        t.t[k].zero_()
+    t.t["p"].fill_(0.5)
+    h = dict(lr=1e-2, b1=0.9, b2=0.95, wd=0.0)
+    tg.tg_adamw([t.t["p"]], [t.t["g"]], [t.t["m"]], [t.t["v"]], 3, h["lr"], betas=(h["b1"], h["b2"]), eps=eps, weight_decay=0.0)
+    m, v = t.t["m"].double(), t.t["v"].double()
+    step = 2.0 ** -149
+    want = (0.05 * t.t["g"].double() ** 2)
+    assert bool(((v - want).abs() <= step / 2 * (1 + 2.0 ** -20) + 4 * U * want).all()) and int((v < 2.0 ** -126).sum()) > n // 2
+    some = v > 0
+    up = h["lr"] / (1 - h["b1"] ** 3) * m / ((v / (1 - h["b2"] ** 3)).sqrt() + eps)
+    w = t.t["p"].double()
+    off = (w - (0.5 - up)).abs() - (12 * U * up.abs() + 4 * U * 0.5 + rounded(0.5 - up, p))
+    assert bool((off[some] <= 0).all()), float(off[some].max())
+
+
+def test_8_bit_roots_of_subnormal_second_moments(tg):
+    """A block whose sqrt(v') is above 2^-100 is held by its roots, though v' is subnormal."""
+    t = Tensor(512, F32, F32, False, True, 1)
+    for k in ("m", "v"):
+        t.t[k].view(torch.uint8).zero_()
+    t.t["g"].fill_(1e-20)
+    t.t["g"][256:] = 3e-21
+    g = t.t["g"][::256].cpu()
+    step_of(tg, [t], 3)
+    omb2 = torch.tensor(1 - 0.95, dtype=torch.float64).float()
+    v = (g * omb2 * g).double()  # (5e-42 and 4.5e-43, each rounded to a multiple of 2^-149)
+    sv = t.t["sv"].cpu().double()
+    assert bool(((sv / (v.sqrt() / 448) - 1).abs() <= 6 * U).all()), sv
+    assert bool((t.t["v"].float() == 448).all())

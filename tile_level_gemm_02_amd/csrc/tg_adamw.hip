@@ -306,15 +306,27 @@ __global__ __launch_bounds__(256) void adamw_step(AdamArgs a)
                     from_e4m3<V>(mq[u], sm[u], m);
                     from_e4m3<V>(vq[u], sv[u], v);
                 }
+                float least = INFINITY;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float g = word_value<G>(gq[u], i) * coef;
-                    const float w0 = word_value<WT>(wq[u], i);
                     const float m0 = EIGHT ? m[i] : bit_cast<float>(mq[u][EIGHT ? 0 : i]);
                     const float v0 = EIGHT ? v[i] * v[i] : bit_cast<float>(vq[u][EIGHT ? 0 : i]);
                     m[i] = m0 * h.b1 + g * h.omb1;
                     v[i] = v0 * h.b2 + g * h.omb2 * g;
                     r[i] = __builtin_amdgcn_sqrtf(v[i]);
+                    least = __builtin_fminf(least, v[i]);
+                }
+                // the instruction takes a subnormal number, whose root is 2^-75 to 2^-63, for 0
+                // (a selection for each value made the step with 8-bit states 1% slower)
+                if (__builtin_amdgcn_ballot_w64(least < 0x1p-126f) != 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        r[i] = v[i] < 0x1p-126f ? __builtin_amdgcn_sqrtf(v[i] * 0x1p64f) * 0x1p-32f : r[i];
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float w0 = word_value<WT>(wq[u], i);
                     w[i] = w0 * h.decay - m[i] * __builtin_amdgcn_rcpf(r[i] * h.root + h.eps) * h.step_size;
                 }
                 uint32_t q[V];
