@@ -113,8 +113,9 @@ int64_t tg_linear_xent_backward_workspace_bytes(tg_input in, int64_t M, int64_t 
  * Tensors must not overlap.  All arithmetic is fp32 on fp32 constants that
  * are computed in fp64; square root and division are off by 2 units in the
  * last place at most together, also of a subnormal v.  step >= 1, betas in
- * [0, 1), eps >= 0, max_norm >= 0 (infinity: no clipping), lr and weight_decay
- * finite, else TG_ERR_INVALID_VALUE. */
+ * [0, 1), eps >= 0 (below 2^-126 it counts as that; 0 makes 0 / 0 of a weight
+ * whose m' and v' are 0), max_norm >= 0 (infinity: no clipping), lr and
+ * weight_decay finite, else TG_ERR_INVALID_VALUE. */
 typedef struct {
     void *param;
     float *master;

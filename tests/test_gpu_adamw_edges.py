@@ -103,3 +103,15 @@ def test_8_bit_roots_of_subnormal_second_moments(tg):
     sv = t.t["sv"].cpu().double()
     assert bool(((sv / (v.sqrt() / 448) - 1).abs() <= 6 * U).all()), sv
     assert bool((t.t["v"].float() == 448).all())
+
+
+@pytest.mark.parametrize("eps", [1e-320, 1e-45, 1e-40, 2.0 ** -126, 1e-30])
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_small_eps_leaves_weights_without_gradients(tg, eps, eight):
+    """m' = v' = 0 over eps > 0 is 0: rows of an embedding that no token took keep their weights."""
+    t = Tensor(600, F32, F32, False, eight, 5)
+    for k in ("g", "m", "v"):
+        t.t[k].view(torch.uint8).zero_()
+    h = dict(exp_avg_scales=[t.t["sm"]], exp_avg_sq_scales=[t.t["sv"]]) if eight else {}
+    tg.tg_adamw([t.t["p"]], [t.t["g"]], [t.t["m"]], [t.t["v"]], 3, 1e-2, eps=eps, weight_decay=0.0, **h)
+    assert torch.equal(t.t["p"], t.before["p"])

@@ -441,7 +441,8 @@ extern "C" tg_status tg_adamw(int64_t count, const tg_adamw_tensor* tensors, int
     h.omb1 = (float)(1.0 - beta1);
     h.b2 = (float)beta2;
     h.omb2 = (float)(1.0 - beta2);
-    h.eps = (float)eps;
+    // (the reciprocal instruction takes a subnormal eps for 0, and 0 / 0 of a weight without gradients for NaN)
+    h.eps = eps > 0.0 && eps < 0x1p-126 ? 0x1p-126f : (float)eps;
     h.lr = lr;
     h.wd = weight_decay;
     h.beta1 = beta1;
