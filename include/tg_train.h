@@ -61,7 +61,7 @@ int64_t tg_linear_xent_workspace_bytes(tg_input in, int64_t M, int64_t V, int64_
  * Each output that is given is overwritten; with M == 0 dW is zero.  Outputs
  * must not overlap inputs or one another.
  * dt is computed in pieces of the vocabulary from logits that are computed
- * again, and rounded to the input type (relative to the largest dloss, for
+ * again, and rounded to the input type (relative to the largest finite dloss, for
  * fp16 2^12 times that, so that small probabilities keep their digits): the
  * 16-bit operand of the two products, whose sums are fp32 over all pieces.
  * An ignored row adds zero times its x to dW: it has to hold finite values.

@@ -549,8 +549,9 @@ struct XentRowsArgs {
 
 constexpr int kXentMost = 32;  // workgroups of xent_most at most: a lane of xent_rows' waves for each
 
-// The largest factor of the rows that count, one for each workgroup; a lane has
-// four rows' loads in flight (131072 rows in one workgroup, a row at a time: 130 us)
+// The largest finite factor of the rows that count, one for each workgroup (an
+// infinite one's row is lost, the others keep their scale); a lane has four rows'
+// loads in flight (131072 rows in one workgroup, a row at a time: 130 us)
 template <int = 0>
 __global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
 {
@@ -575,9 +576,11 @@ __global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (counts[u])
-                most = max2(most, max2(b[u], b[u] * __builtin_fabsf(1.0f + 2.0f * p.z * lse[u])));
+        for (int u = 0; u < 4; ++u) {
+            const float f = max2(b[u], b[u] * __builtin_fabsf(1.0f + 2.0f * p.z * lse[u]));
+            if (counts[u] && f < INFINITY)
+                most = max2(most, f);
+        }
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
@@ -597,7 +600,7 @@ __global__ __launch_bounds__(1024) void xent_most(XentRowsArgs p, float* out)
 template <int = 0>
 __global__ __launch_bounds__(256) void xent_rows(XentRowsArgs p)
 {
-    // 2^e >= most, within fp32's normal numbers (infinity, and none at all: 1)
+    // 2^e >= most, within fp32's normal numbers (none at all: 1)
     int e = 0;
     float most = 1.0f;
     if (p.most != nullptr) {
@@ -607,7 +610,7 @@ __global__ __launch_bounds__(256) void xent_rows(XentRowsArgs p)
         for (int d = kXentMost; d > 0; d >>= 1)
             most = max2(most, __shfl_xor(most, d, 64));
     }
-    if (most > 0.0f && most < INFINITY && most != 1.0f) {
+    if (most > 0.0f && most != 1.0f) {
         (void)frexpf(most, &e);
         e = e < -100 ? -100 : e;
     }
