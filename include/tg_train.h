@@ -39,7 +39,8 @@ extern "C" {
  * Logits and sums are fp32 and are not stored: a product's tile leaves the
  * maximum and the sum of its columns.  A logit of NaN or infinity makes its
  * row's lse and loss NaN (-infinity counts as probability 0).
- * D has to be a multiple of 8, scale and z_loss finite; V > 0 unless M == 0.
+ * D has to be a multiple of 8, scale log2(e) (in fp32) and z_loss finite; V > 0
+ * unless M == 0.
  * The workspace is required when M > 0 or total is given (with M == 0 total
  * receives two zeros); its query holds for M == 0 too. */
 tg_status tg_linear_xent(tg_input in, int64_t M, int64_t V, int64_t D,

@@ -34,3 +34,12 @@ def test_loss_of_no_rows_takes_its_querys_bytes(tg, train, V, D):
     assert call(A, None, 0) == tg.TG_ERR_INVALID_VALUE
     # without a total there is nothing to write, whatever the workspace
     assert call(None, None, 0) == call(None, W, 256) == tg.TG_OK
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38, float("nan")])
+def test_a_scale_whose_exponentials_have_no_fp32_factor(tg, train, scale):
+    """Exponentials are base 2: a scale whose product with log2(e) is past fp32 would make 0 x infinity of a logit of 0."""
+    big = 1 << 40
+    assert train.tg_linear_xent(1, 8, 8, 8, A, 8, A, 8, scale, A, -100, 0.0, A, A, A, W, big, None) == tg.TG_ERR_INVALID_VALUE
+    assert train.tg_linear_xent_backward(1, 8, 8, 8, A, 8, A, 8, scale, A, -100, 0.0, A, A, 1.0, A, A, 8, A, 8, 2, W, big,
+                                         None) == tg.TG_ERR_INVALID_VALUE
