@@ -35,6 +35,8 @@ tg_status tg_quantize_i8(tg_dtype x_dtype, int64_t M, int64_t K, const void *x, 
 /* Y = act(scale_x[m] scale_w[n] (x . W^T) + bias) + residual
  *   x : int8 M x K, W : int8 N x K (the nn.Linear layout); K a multiple of 16
  *       and below 131072, else TG_ERR_NOT_SUPPORTED: the sums are exact int32
+ *       (so are more than 32 rows with 256 ldx + K or 256 ldw + K at 2^31 - 16 or
+ *       above: offsets within a tile are 32 bits wide)
  *   scale_x : fp32 [M], scale_w : fp32 [N];  bias : fp32 [N] or NULL
  *   residual : M x N of y_dtype, or NULL; may be Y itself (same pointer and ld)
  * The sum is rounded to fp32 once, scales, bias, activation and residual are

@@ -41,6 +41,9 @@ extern "C" {
  * row's lse and loss NaN (-infinity counts as probability 0).
  * D has to be a multiple of 8, scale log2(e) (in fp32) and z_loss finite; V > 0
  * unless M == 0.
+ * Offsets within a tile are 32 bits wide: 512 ldx + 2 D and 512 ldw + 2 D have
+ * to be below 2^31 - 16, and for the gradient ldw at most 1398100, else
+ * TG_ERR_NOT_SUPPORTED (and 0 from the queries).
  * The workspace is required when M > 0 or total is given (with M == 0 total
  * receives two zeros); its query holds for M == 0 too. */
 tg_status tg_linear_xent(tg_input in, int64_t M, int64_t V, int64_t D,

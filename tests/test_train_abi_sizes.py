@@ -1,5 +1,5 @@
-"""Sizes that the training operators' queries and validation agree on (CPU
-only: nothing here launches)."""
+"""Sizes and numbers at the ends of what the training operators and the int8
+layers take: queries and refusals (CPU only: nothing here launches)."""
 import pytest
 import torch
 
@@ -43,3 +43,32 @@ def test_a_scale_whose_exponentials_have_no_fp32_factor(tg, train, scale):
     assert train.tg_linear_xent(1, 8, 8, 8, A, 8, A, 8, scale, A, -100, 0.0, A, A, A, W, big, None) == tg.TG_ERR_INVALID_VALUE
     assert train.tg_linear_xent_backward(1, 8, 8, 8, A, 8, A, 8, scale, A, -100, 0.0, A, A, 1.0, A, A, 8, A, 8, 2, W, big,
                                          None) == tg.TG_ERR_INVALID_VALUE
+
+
+def test_rows_too_long_for_32_bit_offsets(tg, train):
+    """The limits that the header states, on their far side; the queries know no leading dimension but the width."""
+    big, bf = 1 << 50, torch.bfloat16
+
+    def loss(D, ldx, ldw):
+        return train.tg_linear_xent(1, 8, 8, D, A, ldx, A, ldw, 1.0, A, -100, 0.0, A, A, A, W, big, None)
+
+    def grad(D, ldx, ldw):
+        return train.tg_linear_xent_backward(1, 8, 8, D, A, ldx, A, ldw, 1.0, A, -100, 0.0, A, A, 1.0, A, A, D, A, D, 2, W, big, None)
+
+    ld = (2 ** 31 - 16 - 16) // 512 // 8 * 8 + 8  # 512 ld + 16 just past the limit
+    assert 512 * ld + 16 >= 2 ** 31 - 16
+    for f in (loss, grad):
+        assert f(8, ld, 8) == f(8, 8, ld) == tg.TG_ERR_NOT_SUPPORTED
+    assert grad(8, 8, 1398104) == tg.TG_ERR_NOT_SUPPORTED
+    assert tg.tg_linear_xent_workspace_bytes(bf, 8, 8, 1 << 22) == tg.tg_linear_xent_backward_workspace_bytes(bf, 8, 8, 1 << 22) == 0
+    assert tg.tg_linear_xent_backward_workspace_bytes(bf, 8, 8, 1398104) == 0 < tg.tg_linear_xent_backward_workspace_bytes(bf, 8, 8, 1398096)
+
+
+def test_int8_rows_too_long_for_32_bit_offsets(tg):
+    from tile_level_gemm_02_amd import int8
+
+    def layer(ldx, ldw):
+        return int8._lib().tg_linear_i8(33, 40, 16, A, ldx, A, ldw, A, A, None, 0, None, 0, A, 40, 2, None, 0, None)
+
+    ld = (2 ** 31 - 16 - 16) // 256 // 16 * 16 + 16
+    assert layer(ld, 16) == layer(16, ld) == tg.TG_ERR_NOT_SUPPORTED
