@@ -48,8 +48,9 @@ def layer(tg, M, N, od, residual):
 
 
 def test_few_rows_and_more_columns_than_a_launch_has_lanes_for(tg):
-    layer(tg, 3, (1 << 27) + 40, BF, False)
-    layer(tg, 20, (1 << 27) + 40, BF, False)
+    for N in ((1 << 28) - 16, (1 << 28) + 40):
+        layer(tg, 3, N, BF, False)
+    layer(tg, 20, (1 << 28) + 40, BF, False)
 
 
 def test_sizes_that_go_in_parts(tg):

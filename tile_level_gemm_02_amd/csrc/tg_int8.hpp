@@ -139,12 +139,13 @@ void launch_i8_skinny(const I8SkinnyArgs<O>& a, int64_t blocks, int split, hipSt
                        dim3((uint32_t)blocks, (uint32_t)split), dim3(64 * WAVES), 0, s, a);
 }
 
-constexpr int kI8MostRing = 4, kI8MostWaves = 8;
+constexpr int kI8MostRing = 4;
 
-// Whether the few-rows kernel takes a call (a launch has less than 2^32 lanes)
+// Whether the few-rows kernel takes a call (a launch has less than 2^32 lanes,
+// and that many workgroups four waves each)
 inline bool i8_skinny(int64_t M, int64_t N, int64_t K)
 {
-    return M <= kI8SkinnyRows && K > 0 && fused_skinny_blocks(M, N) * 64 * kI8MostWaves <= 0x7FFFFFFF;
+    return M <= kI8SkinnyRows && K > 0 && fused_skinny_blocks(M, N) * 64 * 4 < (int64_t)1 << 32;
 }
 
 // Rows of x or W in a launch at most: its tiles, of 512 lanes each, are fewer

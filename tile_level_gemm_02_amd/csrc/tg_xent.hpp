@@ -642,7 +642,7 @@ inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 template <int E>
 bool xent_skinny(int64_t M, int64_t D, int64_t ldx, int64_t ldw, int64_t V)
 {
-    return M <= kFusedSkinnyRows<E> && D > 0 && fused_skinny_blocks(M, V) * 64 * SkinnyCfg::WAVES <= 0x7FFFFFFF &&
+    return M <= kFusedSkinnyRows<E> && D > 0 && fused_skinny_blocks(M, V) * 64 * SkinnyCfg::WAVES < (int64_t)1 << 32 &&
            skinny_offsets_fit(D, ldx, ldw, SkinnyCfg::RING, fused_cg(M, V));
 }
 
