@@ -70,11 +70,12 @@ int64_t tg_linear_xent_workspace_bytes(tg_input in, int64_t M, int64_t V, int64_
  * 16-bit operand of the two products, whose sums are fp32 over all pieces.
  * An ignored row adds zero times its x to dW: it has to hold finite values.
  *
- * The workspace is required (with an output given and V > 0).  Its size sets
- * the pieces: the library takes as few as fit it, and adds dX in another
- * order where that changes them.  workspace_bytes(piece) reports what pieces
- * of `piece` columns need (rounded up to a multiple of 256), for any ldw;
- * piece 0 stands for the size past which more gives nothing, piece 1 for the
+ * The workspace is required (with an output given and V > 0); 128 MiB of it are
+ * for partial sums whatever the sizes.  The rest sets the pieces: the library
+ * takes as few as fit it, and adds dX in another order where that changes them.
+ * workspace_bytes(piece) reports what pieces of `piece` columns need (rounded up
+ * to a multiple of 256), for any ldw; piece 0 stands for the size past which
+ * more gives nothing, piece 1 for the
  * least. */
 tg_status tg_linear_xent_backward(tg_input in, int64_t M, int64_t V, int64_t D,
                                   const void *x, int64_t ldx, const void *W, int64_t ldw,

@@ -8,8 +8,9 @@
 // rows have the same bytes per K step as 16-bit ones with twice the k, so the
 // copies, the ring and the fragments stay as they are and only the matrix
 // instruction (16x16x64, 32x32x32) and the accumulators' type differ.  Bound by
-// the matrix pipe with many rows (8192 x 4096 x 10240 245 us, 2.8 POP/s; a
-// library product of 8192^3 2.14), by fills and epilogues around short loops
+// the matrix pipe with many rows (8192 x 4096 x 10240 246 us, 2.8 POP/s, back to
+// back on the same operands; behind its quantization 243 to 291, by card and
+// clock; a library product of 8192^3 2.0 to 2.5 POP/s), by fills and epilogues around short loops
 // (1003 x 4104 x 2064 with gelu 27 us, 10 of them with a single K step), and by
 // the weight's read with few (1 x 4096 x 4096 5.3 us, 1 x 8192 x 8192 12.4, 5.4
 // TB/s).  The tile plans are fp8's; forced 64, 128, 256 x 128 and 256 tiles ran
