@@ -63,7 +63,8 @@ int64_t tg_linear_xent_workspace_bytes(tg_input in, int64_t M, int64_t V, int64_
  *   dX    : M x D of the input type, or NULL
  *   dW    : V x D of dw_dtype (TG_F32 or the input type), or NULL
  * Each output that is given is overwritten; with M == 0 dW is zero.  Outputs
- * must not overlap inputs or one another.
+ * must not overlap inputs or one another.  grad_scale and scale grad_scale have
+ * to be finite in fp32.
  * dt is computed in pieces of the vocabulary from logits that are computed
  * again, and rounded to the input type (relative to the largest finite dloss, for
  * fp16 2^12 times that, so that small probabilities keep their digits): the

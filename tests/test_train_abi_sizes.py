@@ -72,3 +72,10 @@ def test_int8_rows_too_long_for_32_bit_offsets(tg):
 
     ld = (2 ** 31 - 16 - 16) // 256 // 16 * 16 + 16
     assert layer(ld, 16) == layer(16, ld) == tg.TG_ERR_NOT_SUPPORTED
+
+
+def test_scales_whose_product_is_past_fp32(tg, train):
+    """It is the gradients' common factor: infinite, it would make the zeros of ignored rows NaN."""
+    for scale, gs in ((10.0, 1e38), (-1e20, 1e19), (2.0, -3e38)):
+        assert train.tg_linear_xent_backward(1, 8, 8, 8, A, 8, A, 8, scale, A, -100, 0.0, A, A, gs, A, A, 8, A, 8, 2, W, 1 << 40,
+                                             None) == tg.TG_ERR_INVALID_VALUE

@@ -104,7 +104,8 @@ extern "C" tg_status tg_linear_xent_backward(tg_input in_arg, int64_t M, int64_t
 {
     const int in = abi_int(in_arg), dw_dtype = abi_int(dw_dtype_arg);
     if (M < 0 || V < 0 || D < 0 || in < TG_IN_F16 || in > TG_IN_FP8 || dw_dtype < TG_F32 || dw_dtype > TG_BF16 ||
-        !__builtin_isfinite(xent_c(scale)) || !__builtin_isfinite(z_loss) || !__builtin_isfinite(grad_scale))
+        !__builtin_isfinite(xent_c(scale)) || !__builtin_isfinite(z_loss) || !__builtin_isfinite(grad_scale) ||
+        !__builtin_isfinite((float)((double)scale * (double)grad_scale)))
         return TG_ERR_INVALID_VALUE;
     if (in == TG_IN_FP8 || (dw_dtype != TG_F32 && dw_dtype != (in == TG_IN_F16 ? TG_F16 : TG_BF16)) ||
         !dims_fit(M, V, D, ldx, ldw, lddx) || !dims_fit(lddw, 0, 0))
