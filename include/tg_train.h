@@ -76,8 +76,7 @@ int64_t tg_linear_xent_workspace_bytes(tg_input in, int64_t M, int64_t V, int64_
  * takes as few as fit it, and adds dX in another order where that changes them.
  * workspace_bytes(piece) reports what pieces of `piece` columns need (rounded up
  * to a multiple of 256), for any ldw; piece 0 stands for the size past which
- * more gives nothing, piece 1 for the
- * least. */
+ * more gives nothing, piece 1 for the least. */
 tg_status tg_linear_xent_backward(tg_input in, int64_t M, int64_t V, int64_t D,
                                   const void *x, int64_t ldx, const void *W, int64_t ldw,
                                   float scale, const int64_t *targets, int64_t ignore_index, float z_loss,
@@ -105,10 +104,9 @@ int64_t tg_linear_xent_backward_workspace_bytes(tg_input in, int64_t M, int64_t 
  *               states).  All tensors of a call have one kind of states.
  *   Held in 8 bits, a state's scale is its block's largest finite value / 448 (0,
  *   and the block zeros, below 2^-100), its values are rounded to nearest even
- *   (one that is not finite is held as NaN),
- *   and a nonzero sqrt(v) is kept at e4m3's smallest step or above, so that no
- *   update divides by eps alone.  The update takes the new m and v before they
- *   are rounded.
+ *   (one that is not finite is held as NaN), and a nonzero sqrt(v) is kept at
+ *   e4m3's smallest step or above, so that no update divides by eps alone.  The
+ *   update takes the new m and v before they are rounded.
  *   norm      : device fp32 [1], the gradients' norm as tg_clip_grads writes
  *               it (with max_norm infinity it leaves the gradients as they
  *               are), or NULL.  Where it is NaN or infinite the step changes

@@ -10,15 +10,15 @@
 // lane takes V consecutive values, 4 or 8, so that 64 or 32 lanes hold a block
 // of 8-bit states and its largest value is a reduction between lanes.
 //
-// 300 M bf16 weights with fp32 masters and states 1410 us, 6.0 TB/s; 400 M with
-// 8-bit states 670 us, 6.0 TB/s (a large copy moves 4.7); 9 fp32 tensors of
-// 60 K values 6.6 us, three times a launch that reads one row.  Buffers off 16
-// bytes go a byte at a time: the 300 M, one element off, 6.1 ms.  What got it there: 2048 workgroups that walk the chunks
-// with 32 bytes of each fp32 buffer per lane 2456 and 978 us; one run of whole
-// lines per instruction 1632 and 865; a workgroup for each chunk 1500 and 685;
-// chunks of one unit 1400 with fp32 buffers (two units of 8 values 685, one
-// 692).  Without the non-temporal hint on large loads +3 and +5%, on the
-// stores +4 and +7%.
+// 300 M bf16 weights with fp32 masters and states 1410 us, 6.0 TB/s; 400 M
+// with 8-bit states 670 us, 6.0 TB/s (a large copy moves 4.7); 9 fp32 tensors
+// of 60 K values 6.6 us, three times a launch that reads one row.  Buffers off
+// 16 bytes go a byte at a time: the 300 M, one element off, 6.1 ms.  What got
+// it there: 2048 workgroups that walk the chunks with 32 bytes of each fp32
+// buffer per lane 2456 and 978 us; one run of whole lines per instruction 1632
+// and 865; a workgroup for each chunk 1500 and 685; chunks of one unit 1400
+// with fp32 buffers (two units of 8 values 685, one 692).  Without the non-
+// temporal hint on large loads +3 and +5%, on the stores +4 and +7%.
 #include <math.h>
 
 #include "tg_abi.hpp"

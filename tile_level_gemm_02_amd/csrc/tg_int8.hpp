@@ -10,11 +10,11 @@
 // instruction (16x16x64, 32x32x32) and the accumulators' type differ.  Bound by
 // the matrix pipe with many rows (8192 x 4096 x 10240 246 us, 2.8 POP/s, back to
 // back on the same operands; behind its quantization 243 to 291, by card and
-// clock; a library product of 8192^3 2.0 to 2.5 POP/s), by fills and epilogues around short loops
-// (1003 x 4104 x 2064 with gelu 27 us, 10 of them with a single K step), and by
-// the weight's read with few (1 x 4096 x 4096 5.3 us, 1 x 8192 x 8192 12.4, 5.4
-// TB/s).  The tile plans are fp8's; forced 64, 128, 256 x 128 and 256 tiles ran
-// no faster at any of seven sizes.
+// clock; a library product of 8192^3 2.0 to 2.5 POP/s), by fills and epilogues
+// around short loops (1003 x 4104 x 2064 with gelu 28 us, 10 of them with a
+// single K step), and by the weight's read with few (1 x 4096 x 4096 5.3 us, 1 x
+// 8192 x 8192 12.4, 5.4 TB/s).  The tile plans are fp8's; forced 64, 128, 256 x
+// 128 and 256 tiles ran no faster at any of seven sizes.
 #pragma once
 
 #include "tg_fused.hpp"

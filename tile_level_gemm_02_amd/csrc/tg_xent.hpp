@@ -15,8 +15,8 @@
 // and 6 for the gradient.  Bf16 8192 x 131072 x 4096 5.9 to 6.2 ms forward by
 // card, 1410 to 1490 TFLOP/s (a library product of the same size, which stores its
 // logits, 1490); gradients of 4096 x 128256 x 4096 9.1 to 9.6 ms, 1340 to 1420;
-// 7 x 32000 x 2048 27 us, 4.8 TB/s of the weight; 64 rows 35, 500 rows 65.  The forward epilogue takes 4.5 us a round of 256 tiles,
-// 1.1 of them exponentials.  Smaller tiles (128, 256 x 128) for dt, of which two
+// 7 x 32000 x 2048 27 us, 4.8 TB/s of the weight; 64 rows 35, 500 rows 65.  The
+// forward epilogue takes 4.5 us a round of 256 tiles, 1.1 of them exponentials.  Smaller tiles (128, 256 x 128) for dt, of which two
 // workgroups or a shorter epilogue would overlap, ran 8 to 50% slower at every
 // size tried.
 //
